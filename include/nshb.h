@@ -257,6 +257,51 @@ nshb_status nshb_fro_norms(const nshb_matrix *mats, int32_t n_mats, float *out, 
 #define NSHB_STATIC_SCRATCH_BYTES (4u << 20)
 nshb_status nshb_fro_norms_static(const nshb_matrix *mats, int32_t n_mats, float *out, nshb_stream stream);
 
+/* ------------------------------------------------------------------ lists of tensors
+ * What surrounds a step: the gradients of every parameter before it (matrices, vectors, any
+ * number of them) and the matrices that are quantised to 4 bits after it.
+ * A tensor is rows x cols, row-major with leading dimension ld >= cols (a vector is one row;
+ * ld is not looked at for one row).  rows or cols may be 0: the tensor then has no elements and
+ * its pointer is not looked at.  `data` must be aligned to its element.  Tensors whose rows
+ * follow one another (ld == cols, or one row) are read as one run of elements whatever their
+ * alignment; sizes up to 2^40 elements, ld up to 2^40, else NSHB_ERR_UNSUPPORTED. */
+typedef struct {
+  int64_t rows, cols, ld;
+  int32_t dtype; /* nshb_dtype */
+  int32_t reserved; /* 0 */
+  void *data;
+} nshb_tensor;
+
+/* Bytes of workspace (256-byte aligned) that a call on these tensors needs: the gradients of
+ * nshb_grad_norm and nshb_clip_grads, the sources of nshb_fp4_quantize, the results of
+ * nshb_fp4_matmul.  Host only; depends on the number of tensors alone. */
+nshb_status nshb_tensor_workspace_size(const nshb_tensor *t, int32_t n, size_t *bytes);
+
+typedef enum { NSHB_NORM_L2 = 0, NSHB_NORM_INF = 1 } nshb_norm_kind;
+
+/* The norm of all elements of all tensors taken as one vector, kind NSHB_NORM_L2 (root of the
+ * sum of squares, summed in fp64) or NSHB_NORM_INF (largest magnitude):
+ *   total[0] = norm;  total[1] = min(1, max_norm / (norm + 1e-6)), the factor that clips to max_norm
+ *   each[i]  = the norm of tensor i (each may be NULL)
+ * in fp32 into the DEVICE arrays total (2 floats) and each (n floats).  The same inputs give
+ * the same bits on every call.  An infinite element gives an infinite norm and the factor 0, a NaN
+ * gives NaN for both; either sets NSHB_DEV_NONFINITE in the workspace's status word, which the
+ * call clears otherwise.  max_norm > 0 (infinity: the factor is 1 for every finite norm). */
+nshb_status nshb_grad_norm(const nshb_tensor *g, int32_t n, int32_t kind, float max_norm, float *total, float *each,
+                           void *ws, size_t ws_bytes, nshb_stream stream);
+
+/* nshb_grad_norm, then every element multiplied by total[1] in fp32 and rounded once into
+ * dst[i] (same rows and cols as src[i], any ld and dtype; dst == NULL: in place).  dst[i].data is
+ * either src[i].data (with the same ld and dtype) or does not overlap any source.  Elements between cols and
+ * ld are not written.  In place and with a factor of 1, nothing is written. */
+nshb_status nshb_clip_grads(const nshb_tensor *src, const nshb_tensor *dst, int32_t n, int32_t kind, float max_norm,
+                            float *total, void *ws, size_t ws_bytes, nshb_stream stream);
+
+/* dst[i] = src[i] * *factor (a DEVICE scalar), as in nshb_clip_grads: the second half of a clip
+ * whose norm is formed over several ranks.  No workspace. */
+nshb_status nshb_scale_grads(const nshb_tensor *src, const nshb_tensor *dst, int32_t n, const float *factor,
+                             nshb_stream stream);
+
 /* Synchronises `stream`, then copies the device status word of the last step that used
  * this workspace into *flags (NSHB_DEV_* bits).  The one call that blocks the host. */
 nshb_status nshb_device_status(const void *ws, nshb_stream stream, uint32_t *flags);
@@ -281,7 +326,9 @@ const char *nshb_status_string(int32_t status);
 #define NSHB_PROF_F32GEMM 9  /* fp32 NS GEMMs (all three phases)               */
 #define NSHB_PROF_NEWTON 10  /* Newton-Muon Gram, Cholesky and solves          */
 #define NSHB_PROF_ADAM 11    /* AdamH moments, direction and partials         */
-#define NSHB_PROF_KINDS 12
+#define NSHB_PROF_GRAD 12    /* gradient norms and scaling                    */
+#define NSHB_PROF_FP4 13     /* 4-bit quantisation, values and products       */
+#define NSHB_PROF_KINDS 14
 nshb_status nshb_profile_enable(int32_t on);
 nshb_status nshb_profile_read(int32_t n_kinds, float *ms, int32_t *launches);
 

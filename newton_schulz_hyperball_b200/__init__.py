@@ -20,8 +20,8 @@ from ._abi import (  # noqa: F401  (re-exported constants)
     NSHB_ERR_WORKSPACE, NSHB_ERR_CUDA, NSHB_ERR_DEVICE_TIMEOUT, NSHB_ERR_NONFINITE, NSHB_ERR_ZERO_NORM,
     NSHB_ERR_UNSUPPORTED, NSHB_DEV_ZERO_NORM_FALLBACK, NSHB_DEV_NONFINITE, NSHB_DEV_TIMEOUT,
     NSHB_DEV_ZERO_RADIUS, NSHB_DEV_NOT_SPD, NSHB_OP_MUON, NSHB_OP_HYPERBALL, NSHB_OP_RADIAL_BRAKE,
-    NSHB_OP_HIMUON, NSHB_OP_NEWTON_MUON, NSHB_OP_RELATIVE_UPDATE, NSHB_OP_ADAMH, nshb_matrix, nshb_params,
-    nshb_adam_params,
+    NSHB_OP_HIMUON, NSHB_OP_NEWTON_MUON, NSHB_OP_RELATIVE_UPDATE, NSHB_OP_ADAMH, NSHB_NORM_L2,
+    NSHB_NORM_INF, nshb_matrix, nshb_params, nshb_adam_params, nshb_tensor,
 )
 
 _LIB = None
@@ -301,6 +301,109 @@ def fro_norms_static(mats, out, stream=None):
     import torch
     _device_arg(out, "out", torch.float32, _n(mats))
     _check(lib().nshb_fro_norms_static(mats, _n(mats), _ptr(out), _stream(stream)), "nshb_fro_norms_static")
+
+
+def tensors(ts):
+    """ctypes array of nshb_tensor for a list of CUDA tensors (float32 or bfloat16, one device).
+
+    A tensor is 2-D with unit column stride, or of any shape if contiguous (then one row of its
+    elements).  The array keeps the tensors alive."""
+    arr = (nshb_tensor * max(len(ts), 1))()
+    dev = ts[0].device if len(ts) else None
+    for i, t in enumerate(ts):
+        if t.device != dev or dev.type != "cuda":
+            raise ValueError(f"tensor {i}: every tensor must be on one CUDA device")
+        if t.dim() == 2 and t.numel() and (t.stride(1) == 1 or t.shape[1] == 1) and \
+                (t.stride(0) >= t.shape[1] or t.shape[0] == 1):
+            arr[i].rows, arr[i].cols = t.shape
+            arr[i].ld = max(t.stride(0), t.shape[1])
+        elif t.dim() == 2 and t.numel() == 0:
+            arr[i].rows, arr[i].cols = t.shape
+            arr[i].ld = t.shape[1]
+        elif t.is_contiguous():
+            arr[i].rows, arr[i].cols, arr[i].ld = 1, t.numel(), t.numel()
+        else:
+            raise ValueError(f"tensor {i} must be 2-D with unit column stride, or contiguous")
+        arr[i].dtype = _dtype_code(t)
+        arr[i].data = t.data_ptr()
+    arr._n = len(ts)
+    arr._keep = (list(ts),)
+    arr._device = dev
+    return arr
+
+
+def tensor_workspace(t):
+    """A device workspace for calls on the tensors `t` (see nshb_tensor_workspace_size)."""
+    import torch
+    out = ctypes.c_size_t(0)
+    _check(lib().nshb_tensor_workspace_size(t, _n(t), ctypes.byref(out)), "nshb_tensor_workspace_size")
+    return torch.empty(out.value, dtype=torch.uint8, device=_device_of(t) or "cuda")
+
+
+def _device_of(handle):
+    return getattr(handle, "_device", None)
+
+
+class _On:
+    """Runs a call with the tensors' device current and, unless one is given, its current stream."""
+    __slots__ = ("dev", "stream", "guard")
+
+    def __init__(self, handle, stream, *others):
+        self.dev = _device_of(handle)
+        for what, t in others:
+            d = t.device if hasattr(t, "device") else _device_of(t)
+            if d is not None and self.dev is not None and d != self.dev:
+                raise ValueError(f"{what} is on {d}, the tensors on {self.dev}")
+        self.stream = stream
+
+    def __enter__(self):
+        import torch
+        self.guard = None
+        if self.dev is not None and self.dev.index != torch.cuda.current_device():
+            self.guard = torch.cuda.device(self.dev)
+            self.guard.__enter__()
+        return _stream(self.stream)
+
+    def __exit__(self, *a):
+        if self.guard is not None:
+            self.guard.__exit__(*a)
+
+
+def grad_norm(g, total, ws, max_norm: float = float("inf"), each=None, kind: int = NSHB_NORM_L2, stream=None):
+    """The norm of all elements of the tensors `g` into total[0], and the factor that clips them to
+    `max_norm` into total[1] (CUDA float32 of 2 elements); each[i], when given, the norm of tensor i."""
+    import torch
+    _device_arg(total, "total", torch.float32, 2)
+    _device_arg(each, "each", torch.float32, _n(g))
+    ptr, nbytes = _ws(ws)
+    with _On(g, stream, ("total", total), ("each", each), ("workspace", ws)) as st:
+        _check(lib().nshb_grad_norm(g, _n(g), kind, max_norm, _ptr(total), _ptr(each), ptr, nbytes, st),
+               "nshb_grad_norm")
+
+
+def clip_grads(g, max_norm: float, total, ws, dst=None, kind: int = NSHB_NORM_L2, stream=None):
+    """Scales the tensors `g` so that their norm is at most `max_norm`, in place or into `dst` (a
+    tensors() array of the same sizes, of either dtype); `total` as in grad_norm."""
+    import torch
+    _device_arg(total, "total", torch.float32, 2)
+    _same_count(g, dst)
+    ptr, nbytes = _ws(ws)
+    with _On(g, stream, ("total", total), ("dst", dst), ("workspace", ws)) as st:
+        _check(lib().nshb_clip_grads(g, dst, _n(g), kind, max_norm, _ptr(total), ptr, nbytes, st), "nshb_clip_grads")
+
+
+def scale_grads(g, factor, dst=None, stream=None):
+    """Multiplies the tensors `g` by the one-element CUDA float32 tensor `factor`, in place or into `dst`."""
+    import torch
+    _device_arg(factor, "factor", torch.float32, 1)
+    _same_count(g, dst)
+    with _On(g, stream, ("factor", factor), ("dst", dst)) as st:
+        _check(lib().nshb_scale_grads(g, dst, _n(g), _ptr(factor), st), "nshb_scale_grads")
+
+
+def _same_count(a, b) -> None:
+    if b is not None and _n(a) != _n(b):
+        raise ValueError(f"{_n(b)} destinations for {_n(a)} tensors")
 
 
 def device_status(ws, stream=None) -> int:

@@ -30,8 +30,8 @@ NSHB_DEV_ZERO_RADIUS = 0x8
 NSHB_DEV_NOT_SPD = 0x10
 
 NSHB_PROF_NAMES = ["momentum", "norm", "gram", "poly", "update", "reduce", "finalize", "exact", "apply",
-                   "f32gemm", "newton", "adam"]
-NSHB_PROF_KINDS = 12
+                   "f32gemm", "newton", "adam", "grad", "fp4"]
+NSHB_PROF_KINDS = 14
 
 NSHB_OP_MUON = 0
 NSHB_OP_HYPERBALL = 1
@@ -40,6 +40,9 @@ NSHB_OP_HIMUON = 3
 NSHB_OP_NEWTON_MUON = 4
 NSHB_OP_RELATIVE_UPDATE = 5
 NSHB_OP_ADAMH = 6
+
+NSHB_NORM_L2 = 0
+NSHB_NORM_INF = 1
 
 
 class nshb_matrix(ctypes.Structure):
@@ -87,10 +90,22 @@ class nshb_adam_params(ctypes.Structure):
     ]
 
 
+class nshb_tensor(ctypes.Structure):
+    _fields_ = [
+        ("rows", ctypes.c_int64),
+        ("cols", ctypes.c_int64),
+        ("ld", ctypes.c_int64),
+        ("dtype", ctypes.c_int32),
+        ("reserved", ctypes.c_int32),
+        ("data", ctypes.c_void_p),
+    ]
+
+
 # name -> (restype, argtypes)
 _P = ctypes.c_void_p
 _MATS = ctypes.POINTER(nshb_matrix)
 _PAR = ctypes.POINTER(nshb_params)
+_TENS = ctypes.POINTER(nshb_tensor)
 SIGNATURES = {
     "nshb_default_params": (ctypes.c_int32, [_PAR]),
     "nshb_workspace_size": (ctypes.c_int32, [_MATS, ctypes.c_int32, _PAR, ctypes.c_int32,
@@ -113,6 +128,12 @@ SIGNATURES = {
                                            ctypes.POINTER(ctypes.c_int32)]),
     "nshb_fro_norms": (ctypes.c_int32, [_MATS, ctypes.c_int32, _P, _P, ctypes.c_size_t, _P]),
     "nshb_fro_norms_static": (ctypes.c_int32, [_MATS, ctypes.c_int32, _P, _P]),
+    "nshb_tensor_workspace_size": (ctypes.c_int32, [_TENS, ctypes.c_int32, ctypes.POINTER(ctypes.c_size_t)]),
+    "nshb_grad_norm": (ctypes.c_int32, [_TENS, ctypes.c_int32, ctypes.c_int32, ctypes.c_float, _P, _P, _P,
+                                        ctypes.c_size_t, _P]),
+    "nshb_clip_grads": (ctypes.c_int32, [_TENS, _TENS, ctypes.c_int32, ctypes.c_int32, ctypes.c_float, _P, _P,
+                                         ctypes.c_size_t, _P]),
+    "nshb_scale_grads": (ctypes.c_int32, [_TENS, _TENS, ctypes.c_int32, _P, _P]),
     "nshb_device_status": (ctypes.c_int32, [_P, _P, ctypes.POINTER(ctypes.c_uint32)]),
     "nshb_status_string": (ctypes.c_char_p, [ctypes.c_int32]),
     "nshb_version": (ctypes.c_int32, []),

@@ -348,18 +348,6 @@ int gemm_tiles(int mode, int mt, int nt, int bm, int bn) {
   return cnt;
 }
 
-int device_sms() {
-  static PerDevice cache;
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess) return 148;
-  int v = cache.get(dev);
-  if (!v) {
-    if (cudaDeviceGetAttribute(&v, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || v <= 0) v = 148;
-    cache.set(dev, v);
-  }
-  return v;
-}
-
 #define NSHB_CHECK_CUDA(x)                 \
   do {                                     \
     cudaError_t e_ = (x);                  \
@@ -399,25 +387,11 @@ Profiler &prof() {
   return p;
 }
 struct ProfScope {
-  cudaEvent_t a = nullptr;
+  ProfEvent e;
   int kind;
   cudaStream_t st;
-  ProfScope(int k, cudaStream_t s) : kind(k), st(s) {
-    Profiler &p = prof();
-    if (!p.on) return;
-    std::lock_guard<std::mutex> g(p.mu);
-    a = p.get();
-    if (a) cudaEventRecord(a, st);
-  }
-  ~ProfScope() {
-    if (!a) return;
-    Profiler &p = prof();
-    std::lock_guard<std::mutex> g(p.mu);
-    cudaEvent_t b = p.get();
-    if (!b) return;
-    cudaEventRecord(b, st);
-    p.recs.push_back({a, b, kind});
-  }
+  ProfScope(int k, cudaStream_t s) : e(prof_begin(s)), kind(k), st(s) {}
+  ~ProfScope() { prof_end(e, kind, st); }
 };
 
 #define NSHB_LAUNCH(kind, call)   \
@@ -1330,6 +1304,38 @@ nshb_status check_matrix(const nshb_matrix &d, const float *V, bool need_v, bool
   if (d.O_out && ((uintptr_t)d.O_out % esz) != 0) return NSHB_ERR_SHAPE;
   if ((uintptr_t)d.G % esz || (uintptr_t)d.M % 4 || (uintptr_t)V % 4) return NSHB_ERR_SHAPE;
   return NSHB_OK;
+}
+
+int device_sms() {
+  static PerDevice cache;
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return 148;
+  int v = cache.get(dev);
+  if (!v) {
+    if (cudaDeviceGetAttribute(&v, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || v <= 0) v = 148;
+    cache.set(dev, v);
+  }
+  return v;
+}
+
+ProfEvent prof_begin(cudaStream_t st) {
+  ProfEvent e = {nullptr};
+  Profiler &p = prof();
+  if (!p.on) return e;
+  std::lock_guard<std::mutex> g(p.mu);
+  e.a = p.get();
+  if (e.a) cudaEventRecord(e.a, st);
+  return e;
+}
+
+void prof_end(ProfEvent e, int kind, cudaStream_t st) {
+  if (!e.a) return;
+  Profiler &p = prof();
+  std::lock_guard<std::mutex> g(p.mu);
+  cudaEvent_t b = p.get();
+  if (!b) return;
+  cudaEventRecord(b, st);
+  p.recs.push_back({e.a, b, kind});
 }
 
 void record_cuda_error(cudaError_t e) {

@@ -1,0 +1,392 @@
+// Norm of a list of tensors taken as one vector, and the list multiplied by a scalar: the
+// gradients' global norm and their clipping before an optimizer step.
+//
+//   norm = sqrt(sum x^2)  or  max |x|;   factor = min(1, max_norm / (norm + 1e-6));   y = factor x
+//
+// Both are bound by HBM: every element is read once for the norm, and read and written once for
+// the scaling.  All tensors of a launch form one line of 16 KB windows, split evenly over the
+// CTAs, so that a few vectors and a 12-million-element matrix cost their bytes alone; a CTA
+// keeps its sum in registers and reduces it only where its share of a tensor ends.
+#include <cuda_runtime.h>
+
+#include "nshb_device.cuh"
+#include "nshb_internal.h"
+
+namespace nshb {
+namespace {
+
+constexpr int kThreads = 256;
+
+// The value of one kind over a set: a sum of squares, or the largest magnitude as its bit
+// pattern (magnitudes order as their bits; infinity and NaN are the largest).
+__device__ __forceinline__ double join(int kind, double a, double b) { return kind == kNormL2 ? a + b : fmax(a, b); }
+__device__ __forceinline__ double warp_join(int kind, double v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v = join(kind, v, __shfl_xor_sync(0xffffffffu, v, o));
+  return v;
+}
+
+// Every thread gets the value of the whole block (fixed order); ends with the scratch free.
+__device__ __forceinline__ double block_join(int kind, double v, double *scratch) {
+  v = warp_join(kind, v);
+  __syncthreads();
+  if ((threadIdx.x & 31) == 0) scratch[threadIdx.x >> 5] = v;
+  __syncthreads();
+  double s = scratch[0];
+#pragma unroll
+  for (int w = 1; w < kThreads / 32; ++w) s = join(kind, s, scratch[w]);
+  return s;
+}
+
+__device__ double join_records(int kind, const double *rec, int n, double *scratch) {
+  double v = 0.0;
+  for (int i = threadIdx.x; i < n; i += kThreads) v = join(kind, v, rec[i]);
+  return block_join(kind, v, scratch);
+}
+
+__device__ __forceinline__ float norm_of(int kind, double v) {
+  return kind == kNormL2 ? (float)sqrt(v) : __uint_as_float((uint32_t)v);
+}
+// Not fminf, which would turn a NaN norm into the factor 1.
+__device__ __forceinline__ float factor_of(float norm, float max_norm) {
+  if (isinf(norm)) return 0.f;
+  const float f = max_norm / (norm + 1e-6f);
+  return f > 1.f ? 1.f : f;
+}
+
+__device__ __forceinline__ double square(float x) { return (double)x * (double)x; }
+
+// Eight squares are summed in fp32 (three roundings deep) and the sum is carried in fp64; where the
+// fp32 sum left the range in which no square can have been lost or have overflowed, the
+// eight are summed again in fp64.
+struct SumSquares {
+  double acc = 0.0;
+  __device__ __forceinline__ void add8(const float (&x)[8]) {
+    const float a = fmaf(x[0], x[0], x[1] * x[1]), b = fmaf(x[2], x[2], x[3] * x[3]);
+    const float c = fmaf(x[4], x[4], x[5] * x[5]), d = fmaf(x[6], x[6], x[7] * x[7]);
+    const float s = (a + b) + (c + d);
+    if (s > 1e-20f && s < 1e38f) {
+      acc += (double)s;
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) acc += square(x[e]);
+    }
+  }
+  __device__ __forceinline__ void add1(float x) { acc += square(x); }
+  __device__ __forceinline__ double value() const { return acc; }
+};
+template <bool FINITE>
+struct LargestBits {
+  uint32_t top = 0;
+  __device__ __forceinline__ void add1(float x) {
+    const uint32_t b = __float_as_uint(x) & 0x7fffffffu;
+    if (!FINITE || b < 0x7f800000u) top = top > b ? top : b;
+  }
+  __device__ __forceinline__ void add8(const float (&x)[8]) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) add1(x[e]);
+  }
+  __device__ __forceinline__ double value() const { return (double)top; }
+};
+
+template <bool F32>
+__device__ __forceinline__ float load1(const void *p, int64_t i) {
+  if (F32) return static_cast<const float *>(p)[i];
+  return bf16lo((uint32_t) static_cast<const unsigned short *>(p)[i]);
+}
+template <bool F32>
+__device__ __forceinline__ void store1(void *p, int64_t i, float x) {
+  if (F32) static_cast<float *>(p)[i] = x;
+  else static_cast<__nv_bfloat16 *>(p)[i] = __float2bfloat16_rn(x);
+}
+
+// A thread's share of a window: 64 bytes, E elements.
+template <bool F32>
+struct Share {
+  static constexpr int E = F32 ? 16 : 32;
+  uint32_t w[16];
+  __device__ __forceinline__ void load(const void *p) {
+    uint32_t a[8], b[8];
+    ld_global_256(p, a);
+    ld_global_256(static_cast<const char *>(p) + 32, b);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      w[e] = a[e];
+      w[8 + e] = b[e];
+    }
+  }
+  __device__ __forceinline__ float get(int e) const {
+    if (F32) return __uint_as_float(w[e]);
+    return (e & 1) ? bf16hi(w[e >> 1]) : bf16lo(w[e >> 1]);
+  }
+};
+
+// Where window `win` of a run puts this thread: the run's row and the first of its E elements
+// (negative or past the row's end in the partial windows).
+struct Place {
+  int row;
+  int64_t at;
+  bool whole;
+};
+template <bool F32>
+__device__ __forceinline__ Place place(const TensRec &q, int win) {
+  constexpr int E = Share<F32>::E, W = kWinBytes / (F32 ? 4 : 2);
+  Place r;
+  int k = win;
+  r.row = 0;
+  if (q.rows > 1) {
+    r.row = win / q.per_row;
+    k = win - r.row * q.per_row;
+  }
+  const uintptr_t base = reinterpret_cast<uintptr_t>(q.src) + (uintptr_t)((int64_t)r.row * q.sld * (F32 ? 4 : 2));
+  r.at = (int64_t)k * W - (int64_t)((base & 31) / (F32 ? 4 : 2)) + (int64_t)threadIdx.x * E;
+  r.whole = r.at >= 0 && r.at + E <= q.cols;
+  return r;
+}
+template <bool F32>
+__device__ __forceinline__ const char *run_ptr(const TensRec &q, const Place &l) {
+  return static_cast<const char *>(q.src) + ((int64_t)l.row * q.sld + l.at) * (F32 ? 4 : 2);
+}
+
+template <class V, bool F32>
+__device__ __forceinline__ double norm_windows(const TensRec &q, int w, int wend) {
+  V v;
+  if (q.flags & kTensRun) {
+    auto add = [&](const Share<F32> &s) {
+#pragma unroll
+      for (int g = 0; g < Share<F32>::E / 8; ++g) {
+        float x[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[e] = s.get(8 * g + e);
+        v.add8(x);
+      }
+    };
+    auto one = [&](const Place &l) {
+      if (l.whole) {
+        Share<F32> s;
+        s.load(run_ptr<F32>(q, l));
+        add(s);
+      } else {
+        const char *row = static_cast<const char *>(q.src) + (int64_t)l.row * q.sld * (F32 ? 4 : 2);
+        const int64_t lo = l.at > 0 ? l.at : 0;
+        const int64_t hi = l.at + Share<F32>::E < q.cols ? l.at + Share<F32>::E : q.cols;
+        for (int64_t i = lo; i < hi; ++i) v.add1(load1<F32>(row, i));
+      }
+    };
+    // two windows at a time: 128 bytes of each thread in flight
+    for (; w + 1 < wend; w += 2) {
+      const Place l0 = place<F32>(q, w), l1 = place<F32>(q, w + 1);
+      if (l0.whole && l1.whole) {
+        Share<F32> s0, s1;
+        s0.load(run_ptr<F32>(q, l0));
+        s1.load(run_ptr<F32>(q, l1));
+        add(s0);
+        add(s1);
+      } else {
+        one(l0);
+        one(l1);
+      }
+    }
+    if (w < wend) one(place<F32>(q, w));
+  } else {
+    for (; w < wend; ++w) {
+      const int r0 = w * q.per_row, cols = (int)q.cols;
+      const int nr = q.rows - r0 < q.per_row ? q.rows - r0 : q.per_row;
+      for (int i = threadIdx.x; i < nr * cols; i += kThreads) {
+        const int r = i / cols;
+        v.add1(load1<F32>(q.src, (int64_t)(r0 + r) * q.sld + (i - r * cols)));
+      }
+    }
+  }
+  return v.value();
+}
+
+__device__ __forceinline__ int find_tensor(const TensParams &p, int win) {
+  int lo = 0, hi = p.ntens - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (p.t[mid].win_begin <= win) lo = mid; else hi = mid - 1;
+  }
+  return lo;
+}
+
+// CTA c takes windows [c nwin / nctas, (c + 1) nwin / nctas) and writes one record per tensor that
+// it meets, at index c + t.  Along the line c + t grows by one at every border of a CTA's share or of a
+// tensor; where both borders meet it grows by two, and the record between is set to zero.  So the
+// records are a list without gaps in a fixed order, tensor t's are consecutive, and their number does
+// not depend on the sizes.
+template <class V>
+__device__ __forceinline__ void norm_line(const TensParams &p) {
+  __shared__ double scratch[kThreads / 32];
+  const int c = blockIdx.x;
+  const int w0 = (int)((int64_t)c * p.nwin / p.nctas), w1 = (int)((int64_t)(c + 1) * p.nwin / p.nctas);
+  int t = find_tensor(p, w0);
+  for (int w = w0; w < w1; ++t) {
+    const TensRec &q = p.t[t];
+    const int tend = t + 1 < p.ntens ? p.t[t + 1].win_begin : p.nwin;
+    const int wend = tend < w1 ? tend : w1;
+    const int a = w - q.win_begin, b = wend - q.win_begin;
+    const double v = (q.flags & kTensF32) ? norm_windows<V, true>(q, a, b) : norm_windows<V, false>(q, a, b);
+    const double s = block_join(p.kind, v, scratch);
+    if (threadIdx.x == 0) {
+      p.rec[c + t] = s;
+      if (wend == tend && wend == w1 && t + 1 < p.ntens) p.rec[c + t + 1] = 0.0;
+    }
+    w = wend;
+  }
+}
+
+__global__ void __launch_bounds__(kThreads, kNormCtasPerSm) tens_norm_kernel(const __grid_constant__ TensParams p) {
+  pdl_trigger();
+  pdl_wait();
+  if (p.kind == kNormL2) norm_line<SumSquares>(p);
+  else if (p.kind == kNormInf) norm_line<LargestBits<false>>(p);
+  else norm_line<LargestBits<true>>(p);
+}
+
+// One CTA: the norms of the tensors (where asked for) and of the whole.
+__global__ void __launch_bounds__(kThreads) tens_finalize_kernel(const __grid_constant__ TensFinParams p) {
+  __shared__ double scratch[kThreads / 32];
+  pdl_trigger();
+  pdl_wait();
+  if (p.each) {
+    const int lane = threadIdx.x & 31;
+    for (int k = threadIdx.x >> 5; k < p.ntens; k += kThreads / 32) {
+      const int c0 = win_cta(p.win_begin[k], p.nwin, p.nctas), c1 = win_cta(p.win_begin[k + 1] - 1, p.nwin, p.nctas);
+      double v = 0.0;
+      for (int c = c0 + lane; c <= c1; c += 32) v = join(p.kind, v, p.rec[c + k]);
+      v = warp_join(p.kind, v);
+      if (lane == 0) p.each[p.index[k]] = norm_of(p.kind, v);
+    }
+    for (int k = p.ntens + threadIdx.x; k < p.ntens + p.n_empty; k += kThreads) p.each[p.index[k]] = 0.f;
+  }
+  double v = join_records(p.kind, p.rec, p.ntens ? p.nctas + p.ntens - 1 : 0, scratch);
+  if (threadIdx.x == 0) {
+    if (!p.first) v = join(p.kind, *p.acc, v);
+    if (!p.last) {
+      *p.acc = v;
+    } else {
+      const float norm = norm_of(p.kind, v);
+      p.total[0] = norm;
+      p.total[1] = factor_of(norm, p.max_norm);
+      *p.status = isfinite(norm) ? 0u : NSHB_DEV_NONFINITE;
+    }
+  }
+}
+
+// Stores E = 8 N fp32 values, rounded to the destination's type, with the widest accesses its
+// address allows.
+template <bool DF32, int E>
+__device__ __forceinline__ void store_share(char *d, const float (&y)[E]) {
+  constexpr int NW = DF32 ? E : E / 2;
+  const uintptr_t a = reinterpret_cast<uintptr_t>(d);
+  if ((a & 15) == 0) {
+    uint32_t w[NW];
+#pragma unroll
+    for (int e = 0; e < NW; ++e) w[e] = DF32 ? __float_as_uint(y[e]) : pack_bf16(y[2 * e], y[2 * e + 1]);
+    if ((a & 31) == 0) {
+#pragma unroll
+      for (int g = 0; g < NW / 8; ++g) {
+        uint32_t o[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) o[e] = w[8 * g + e];
+        st_global_256(d + 32 * g, o);
+      }
+    } else {
+#pragma unroll
+      for (int g = 0; g < NW / 4; ++g)
+        *reinterpret_cast<uint4 *>(d + 16 * g) = make_uint4(w[4 * g], w[4 * g + 1], w[4 * g + 2], w[4 * g + 3]);
+    }
+  } else {
+#pragma unroll
+    for (int e = 0; e < E; ++e) store1<DF32>(d, e, y[e]);
+  }
+}
+
+template <bool F32, bool DF32>
+__device__ __forceinline__ void scale_windows(const TensRec &q, int w, int wend, float f) {
+  constexpr int E = Share<F32>::E;
+  // backwards: the windows that the norm read last are still in the L2 cache
+  if (q.flags & kTensRun) {
+    for (int u = wend - 1; u >= w; --u) {
+      const Place l = place<F32>(q, u);
+      char *drow = static_cast<char *>(q.dst) + (int64_t)l.row * q.dld * (DF32 ? 4 : 2);
+      if (l.whole) {
+        Share<F32> s;
+        s.load(run_ptr<F32>(q, l));
+        float y[E];
+#pragma unroll
+        for (int e = 0; e < E; ++e) y[e] = f * s.get(e);
+        store_share<DF32, E>(drow + l.at * (DF32 ? 4 : 2), y);
+      } else {
+        const char *row = static_cast<const char *>(q.src) + (int64_t)l.row * q.sld * (F32 ? 4 : 2);
+        const int64_t lo = l.at > 0 ? l.at : 0, hi = l.at + E < q.cols ? l.at + E : q.cols;
+        for (int64_t i = lo; i < hi; ++i) store1<DF32>(drow, i, f * load1<F32>(row, i));
+      }
+    }
+  } else {
+    for (int u = wend - 1; u >= w; --u) {
+      const int r0 = u * q.per_row, cols = (int)q.cols;
+      const int nr = q.rows - r0 < q.per_row ? q.rows - r0 : q.per_row;
+      for (int i = threadIdx.x; i < nr * cols; i += kThreads) {
+        const int r = i / cols, j = i - r * cols;
+        store1<DF32>(q.dst, (int64_t)(r0 + r) * q.dld + j, f * load1<F32>(q.src, (int64_t)(r0 + r) * q.sld + j));
+      }
+    }
+  }
+}
+
+// The factor is read, or formed from the norm's records by every CTA for itself (a few KB from L2,
+// no launch between the norm and the scaling).
+__global__ void __launch_bounds__(kThreads, kScaleCtasPerSm) tens_scale_kernel(const __grid_constant__ TensParams p) {
+  __shared__ double scratch[kThreads / 32];
+  pdl_trigger();
+  pdl_wait();
+  float f;
+  if (p.coef_rec) {
+    const float norm = norm_of(p.kind, join_records(p.kind, p.coef_rec, p.n_rec, scratch));
+    f = factor_of(norm, p.max_norm);
+    if (blockIdx.x == 0 && threadIdx.x == 0) {
+      p.total[0] = norm;
+      p.total[1] = f;
+      *p.status = isfinite(norm) ? 0u : NSHB_DEV_NONFINITE;
+    }
+  } else {
+    f = *p.factor;
+  }
+  const int c = blockIdx.x;
+  const int w0 = (int)((int64_t)c * p.nwin / p.nctas), w1 = (int)((int64_t)(c + 1) * p.nwin / p.nctas);
+  for (int t = find_tensor(p, w1 - 1), w = w1; w > w0; --t) {
+    const TensRec &q = p.t[t];
+    const int wb = q.win_begin > w0 ? q.win_begin : w0;
+    const int a = wb - q.win_begin, b = w - q.win_begin;
+    const bool still = f == 1.f && q.src == q.dst;   // in place: the values stay as they are
+    if (!still) {
+      switch (q.flags & (kTensF32 | kTensDstF32)) {
+        case 0: scale_windows<false, false>(q, a, b, f); break;
+        case kTensF32: scale_windows<true, false>(q, a, b, f); break;
+        case kTensDstF32: scale_windows<false, true>(q, a, b, f); break;
+        default: scale_windows<true, true>(q, a, b, f); break;
+      }
+    }
+    w = wb;
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_tens_norm(const TensParams &p, cudaStream_t s) {
+  if (p.nwin <= 0) return cudaSuccess;
+  return launch_pdl(tens_norm_kernel, dim3(p.nctas), dim3(kThreads), 0, s, p);
+}
+
+cudaError_t launch_tens_finalize(const TensFinParams &p, cudaStream_t s) {
+  return launch_pdl(tens_finalize_kernel, dim3(1), dim3(kThreads), 0, s, p);
+}
+
+cudaError_t launch_tens_scale(const TensParams &p, cudaStream_t s) {
+  if (p.nwin <= 0) return cudaSuccess;
+  return launch_pdl(tens_scale_kernel, dim3(p.nctas), dim3(kThreads), 0, s, p);
+}
+
+}  // namespace nshb

@@ -275,6 +275,13 @@ struct CholParams {          // the ridge of a batch of layer-input Gram matrice
 nshb_status check_matrix(const nshb_matrix &d, const float *V = nullptr, bool need_v = false, bool w_only = false);
 // Records a CUDA error for nshb_last_cuda_error (per calling thread) and clears it.
 void record_cuda_error(cudaError_t e);
+int device_sms();
+// Brackets a launch with the events of nshb_profile_enable (see ProfScope in api.cu).
+struct ProfEvent {
+  cudaEvent_t a;
+};
+ProfEvent prof_begin(cudaStream_t st);
+void prof_end(ProfEvent e, int kind, cudaStream_t st);
 
 // Split-precision (bf16 x 3) products of the Newton-Muon preconditioner (newton_tc.cu):
 // D = A B^T (B K-major), D = A B (B MN-major) or D = C - A B^(T), over 256 x 256 tiles of
@@ -339,6 +346,58 @@ struct DiagParams {
   int32_t ld[kMaxMats];            // S row stride = panel height of the inverse stack
 };
 
+// Lists of tensors (grad_norm.cu).  A tensor is cut into windows of kWinBytes source bytes; the
+// windows of a launch form one line that is split evenly over the CTAs.  A tensor whose elements
+// follow one another is one run: its windows start on 32-byte boundaries of the address, so the
+// first and the last may be partial.  Rows of kLongRow elements or more are a run each; shorter
+// rows are taken several to a window, element by element.
+constexpr int kWinBytes = 16384;
+constexpr int kMaxTens = 512;
+constexpr int kLongRow = 256;
+constexpr int kNormCtasPerSm = 3;    // 128 bytes of each thread in flight, 85 registers
+constexpr int kScaleCtasPerSm = 4;   // 64 bytes, 64 registers
+constexpr int kTensF32 = 1;      // source is fp32 (else bf16)
+constexpr int kTensDstF32 = 2;   // destination is fp32 (else bf16)
+constexpr int kTensRun = 4;      // windows of runs (else several short rows to a window)
+struct TensRec {
+  const void *src;
+  void *dst;
+  int64_t cols;            // elements of a run / of a row
+  int64_t sld, dld;
+  int32_t rows;            // runs, or short rows
+  int32_t win_begin;       // first window of this tensor in the launch
+  int32_t per_row;         // kTensRun: windows a run; else rows a window
+  int32_t flags;
+};
+struct TensParams {
+  double *rec;             // norm: one record per (CTA, tensor) step of the line, see tens_norm_kernel
+  const double *coef_rec;  // scale: the records of the whole set (factor formed from them), or NULL
+  const float *factor;     // scale: the factor, where coef_rec is NULL
+  float *total;            // scale with coef_rec: norm and factor, written by the first CTA
+  uint32_t *status;
+  float max_norm;
+  int32_t kind;            // kNormL2 ...
+  int32_t n_rec;           // records behind coef_rec
+  int32_t ntens, nwin, nctas;
+  TensRec t[kMaxTens];
+};
+enum NormKind { kNormL2 = 0, kNormInf = 1, kNormFinite = 2 };   // kNormFinite: largest finite magnitude
+struct TensFinParams {
+  const double *rec;       // records of this launch's tensors
+  double *acc;             // the running value over the launches of one call
+  float *total, *each;
+  uint32_t *status;
+  float max_norm;
+  int32_t kind, first, last;
+  int32_t ntens, n_empty, nwin, nctas;
+  int32_t win_begin[kMaxTens + 1];
+  int32_t index[kMaxTens]; // where tensor k's norm goes in `each`; the last n_empty have no elements
+};
+// The CTA of `nctas` that takes window w of a line of nwin: CTA c takes [c nwin / nctas, (c + 1) nwin / nctas).
+__host__ __device__ inline int win_cta(int w, int nwin, int nctas) {
+  return (int)((((int64_t)w + 1) * nctas - 1) / nwin);
+}
+
 // Launchers (defined in the .cu files); each returns cudaGetLastError().
 cudaError_t launch_momentum(const MomentumParams &p, cudaStream_t s);
 cudaError_t launch_norm_finalize(const NormFinParams &p, int nseg_total, cudaStream_t s);
@@ -366,6 +425,10 @@ cudaError_t launch_newton_gemm(const NwParams &p, int num_sms, cudaStream_t s, i
 cudaError_t launch_split(const SplitParams &p, cudaStream_t s);
 cudaError_t launch_potrf_diag(const DiagParams &p, cudaStream_t s);
 
+cudaError_t launch_tens_norm(const TensParams &p, cudaStream_t s);
+cudaError_t launch_tens_finalize(const TensFinParams &p, cudaStream_t s);
+cudaError_t launch_tens_scale(const TensParams &p, cudaStream_t s);
+
 constexpr size_t kMaxParamBytes = 32764;   // kernel parameter limit (CUDA 12.1+, sm_70+)
 static_assert(sizeof(MomentumParams) <= kMaxParamBytes, "MomentumParams");
 static_assert(sizeof(NormFinParams) <= kMaxParamBytes, "NormFinParams");
@@ -379,6 +442,8 @@ static_assert(sizeof(SyrkParams) <= kMaxParamBytes, "SyrkParams");
 static_assert(sizeof(CholParams) <= kMaxParamBytes, "CholParams");
 static_assert(sizeof(NwParams) <= kMaxParamBytes, "NwParams");
 static_assert(sizeof(SplitParams) <= kMaxParamBytes, "SplitParams");
+static_assert(sizeof(TensParams) <= kMaxParamBytes, "TensParams");
+static_assert(sizeof(TensFinParams) <= kMaxParamBytes, "TensFinParams");
 static_assert(sizeof(DiagParams) <= kMaxParamBytes, "DiagParams");
 
 }  // namespace nshb

@@ -1,0 +1,37 @@
+// What the entry points on lists of tensors share (host side).
+#pragma once
+#include <cstddef>
+
+#include "../../include/nshb.h"
+#include "nshb_internal.h"
+
+#define NSHB_RUN(kind, call)                          \
+  do {                                                \
+    const ::nshb::ProfEvent pe_ = ::nshb::prof_begin(st); \
+    const cudaError_t e_ = (call);                    \
+    ::nshb::prof_end(pe_, kind, st);                  \
+    if (e_ != cudaSuccess) {                          \
+      ::nshb::record_cuda_error(e_);                  \
+      return NSHB_ERR_CUDA;                           \
+    }                                                 \
+  } while (0)
+
+namespace nshb {
+
+constexpr int kMaxTensCtas = 1024;   // records per launch: at most this many CTAs + kMaxTens
+
+// The workspace of a call on a list of tensors: [0, 256) the status word and the running value of
+// a norm that takes several launches, then the records of one launch.
+struct TensWorkspace {
+  uint32_t *status;
+  double *acc;
+  double *rec;
+  size_t bytes;
+};
+TensWorkspace tens_workspace(void *ws, int32_t n);
+nshb_status check_tens_ws(void *ws, size_t bytes, int32_t n);
+nshb_status check_tensor(const nshb_tensor &t);
+nshb_status check_tensors(const nshb_tensor *t, int32_t n);
+int tens_ctas(int nwin, int per_sm);
+
+}  // namespace nshb

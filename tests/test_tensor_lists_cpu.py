@@ -1,0 +1,100 @@
+"""Refusals of the entry points on lists of tensors: returned before any CUDA call (CPU only)."""
+import ctypes
+
+import pytest
+import torch
+
+import newton_schulz_hyperball_b200 as nshb
+
+TOTAL = 0x7000000
+WS = 0x8000000
+
+
+def fake(*shapes, dtype=nshb.NSHB_BF16, base=0x10000000):
+    arr = (nshb.nshb_tensor * max(len(shapes), 1))()
+    for i, (r, c) in enumerate(shapes):
+        arr[i].rows, arr[i].cols, arr[i].ld, arr[i].dtype = r, c, c, dtype
+        arr[i].data = base + 0x1000000 * i
+    arr._n = len(shapes)
+    return arr
+
+
+def size(t, n=None):
+    out = ctypes.c_size_t(0)
+    return nshb.lib().nshb_tensor_workspace_size(t, t._n if n is None else n, ctypes.byref(out)), out.value
+
+
+def norm(t, kind=0, max_norm=1.0, total=TOTAL, each=None, ws=WS, ws_bytes=1 << 20, n=None):
+    return nshb.lib().nshb_grad_norm(t, t._n if n is None else n, kind, max_norm, total, each, ws, ws_bytes, None)
+
+
+def clip(s, d=None, kind=0, max_norm=1.0, total=TOTAL, ws=WS, ws_bytes=1 << 20):
+    return nshb.lib().nshb_clip_grads(s, d, s._n, kind, max_norm, total, ws, ws_bytes, None)
+
+
+def test_struct_layout():
+    assert ctypes.sizeof(nshb.nshb_tensor) == 40 and nshb.nshb_tensor.data.offset == 32
+
+
+def test_workspace_grows_with_the_number_of_tensors_alone():
+    few, many = size(fake((2, 3)))[1], size(fake(*[(2, 3)] * 300))[1]
+    assert 256 < few < many <= size(fake(*[(20000, 30000)] * 300))[1] == many
+    assert many % 256 == 0 and size(fake())[0] == nshb.NSHB_OK
+
+
+@pytest.mark.parametrize("change,code", [
+    (dict(rows=-1), nshb.NSHB_ERR_SHAPE),
+    (dict(cols=-1), nshb.NSHB_ERR_SHAPE),
+    (dict(ld=4), nshb.NSHB_ERR_SHAPE),
+    (dict(data=0x10000001), nshb.NSHB_ERR_SHAPE),
+    (dict(rows=(1 << 40) + 1), nshb.NSHB_ERR_UNSUPPORTED),
+    (dict(rows=1 << 21, cols=1 << 20, ld=1 << 20), nshb.NSHB_ERR_UNSUPPORTED),
+    (dict(ld=(1 << 40) + 1), nshb.NSHB_ERR_UNSUPPORTED),
+    (dict(dtype=2), nshb.NSHB_ERR_DTYPE),
+    (dict(reserved=1), nshb.NSHB_ERR_PARAM),
+    (dict(data=None), nshb.NSHB_ERR_NULL),
+])
+def test_a_bad_tensor_is_refused_everywhere(change, code):
+    t = fake((3, 5), (2, 5), (4, 5))
+    for k, v in change.items():
+        setattr(t[1], k, v)
+    good = fake((3, 5), (2, 5), (4, 5), base=0x20000000)
+    assert size(t)[0] == norm(t) == clip(t) == clip(good, t) == code
+    assert nshb.lib().nshb_scale_grads(t, None, 3, TOTAL, None) == code
+    assert nshb.lib().nshb_scale_grads(good, t, 3, TOTAL, None) == code
+
+
+def test_bad_arguments():
+    t = fake((3, 5))
+    assert norm(t, n=-1) == size(t, -1)[0] == nshb.NSHB_ERR_SHAPE
+    assert norm(t, total=None) == clip(t, total=None) == norm(t, ws=None) == nshb.NSHB_ERR_NULL
+    assert nshb.lib().nshb_grad_norm(None, 1, 0, 1.0, TOTAL, None, WS, 1 << 20, None) == nshb.NSHB_ERR_NULL
+    assert nshb.lib().nshb_tensor_workspace_size(t, 1, None) == nshb.NSHB_ERR_NULL
+    assert nshb.lib().nshb_scale_grads(t, None, 1, None, None) == nshb.NSHB_ERR_NULL
+    assert nshb.lib().nshb_scale_grads(t, None, 1, TOTAL + 2, None) == nshb.NSHB_ERR_SHAPE
+    assert norm(t, total=TOTAL + 2) == norm(t, each=TOTAL + 1) == nshb.NSHB_ERR_SHAPE
+    for bad in (0.0, -1.0, float("nan")):
+        assert norm(t, max_norm=bad) == clip(t, max_norm=bad) == nshb.NSHB_ERR_PARAM
+    assert norm(t, kind=2) == clip(t, kind=-1) == nshb.NSHB_ERR_PARAM
+    need = size(t)[1]
+    assert norm(t, ws_bytes=need - 1) == clip(t, ws_bytes=need - 1) == norm(t, ws=WS + 128) == nshb.NSHB_ERR_WORKSPACE
+
+
+def test_bad_destinations():
+    s = fake((3, 5), (2, 5))
+    assert clip(s, fake((3, 5), (2, 6), base=0x20000000)) == nshb.NSHB_ERR_SHAPE
+    assert clip(s, fake((3, 5), (5, 2), base=0x20000000)) == nshb.NSHB_ERR_SHAPE
+    assert clip(s, fake((3, 5), (2, 5), dtype=nshb.NSHB_F32)) == nshb.NSHB_ERR_PARAM     # in place, another type
+    d = fake((3, 5), (2, 5))
+    d[1].ld = 6
+    assert clip(s, d) == nshb.NSHB_ERR_PARAM                                             # in place, another layout
+
+
+def test_the_binding_refuses_what_the_library_cannot_see():
+    with pytest.raises(ValueError, match="CUDA"):
+        nshb.tensors([torch.zeros(3)])
+    t = fake((3, 5))
+    with pytest.raises(ValueError, match="CUDA"):
+        nshb.grad_norm(t, torch.zeros(2), (WS, 1 << 20))
+    with pytest.raises(ValueError, match="2 destinations for 1"):
+        nshb.clip_grads(t, 1.0, TOTAL, (WS, 1 << 20), dst=fake((3, 5), (3, 5)))
