@@ -302,6 +302,47 @@ nshb_status nshb_clip_grads(const nshb_tensor *src, const nshb_tensor *dst, int3
 nshb_status nshb_scale_grads(const nshb_tensor *src, const nshb_tensor *dst, int32_t n, const float *factor,
                              nshb_stream stream);
 
+/* ------------------------------------------------- microscaled 4-bit floating point
+ * A rows x cols matrix of E2M1 codes (sign, 0, 0.5, 1, 1.5, 2, 3, 4, 6) with a scale per block of
+ * consecutive columns of a row:
+ *   NSHB_MXFP4  32 columns, scale a power of two (E8M0: 2^(byte - 127), 255 = NaN);
+ *               exponent floor(log2(largest magnitude)) - 2 ("OCP Microscaling Formats (MX)
+ *               Specification" v1.0, section 6.3), so magnitudes over 6 scales round to 6;
+ *   NSHB_NVFP4  16 columns, scale E4M3 (0x7F = NaN) and one fp32 scale for the matrix (*global, DEVICE):
+ *               *global is the smallest power of two with largest magnitude <= 448 * 6 * *global (at
+ *               least 2^-126; 1 for a zero matrix), a block's scale its largest magnitude / (6 * *global)
+ *               rounded to E4M3.
+ * value = code * scale (* *global).  A code is the nearest to x / (scale * *global), ties to the even
+ * code, exactly (no intermediate rounding decides).  A block with a NaN or infinity gets the scale
+ * NaN and zero codes; it does not count for *global.  Subnormal inputs are read as they are.
+ *
+ * codes:  rows of round_up(cols, 128) / 2 bytes, column 2j in the low half of byte j; 16-byte
+ *         aligned; zero past cols.
+ * scales: tiles of 128 rows x 4 scales (512 bytes, 16-byte aligned), tile (i, j) at index
+ *         i * tiles_per_row + j with tiles_per_row = round_up(cols, 128) / (4 * block); scale (r, s) of a
+ *         tile at byte 16 (r mod 32) + 4 (r div 32) + s: the order in which the tensor core reads them.
+ * nshb_fp4_size gives the bytes of both.  rows and cols up to 2^24; 0 allowed (nothing is read or written). */
+typedef enum { NSHB_MXFP4 = 0, NSHB_NVFP4 = 1 } nshb_fp4_format;
+typedef struct {
+  int64_t rows, cols;
+  int32_t format;   /* nshb_fp4_format */
+  int32_t reserved; /* 0 */
+  void *codes;
+  void *scales;
+  float *global;    /* NSHB_NVFP4 only */
+} nshb_fp4;
+nshb_status nshb_fp4_size(int64_t rows, int64_t cols, int32_t format, size_t *code_bytes, size_t *scale_bytes);
+
+/* Q[i] = the 4-bit form of X[i] (bf16 or fp32), or with `transpose` of its transpose (Q[i] then has X[i]'s
+ * cols as rows): the weights a step left, for the products of the next forward (W) and backward (W^T)
+ * pass; a layer's input, tokens x features, as the features x tokens operand of newton_muon_step_fp4.
+ * ws: nshb_tensor_workspace_size(X, n) bytes, needed (and looked at) only if some Q[i] is NSHB_NVFP4. */
+nshb_status nshb_fp4_quantize(const nshb_tensor *X, const nshb_fp4 *Q, int32_t n, int32_t transpose, void *ws,
+                              size_t ws_bytes, nshb_stream stream);
+
+/* X[i] = the values of Q[i] (same rows and cols), rounded once to X[i]'s dtype. */
+nshb_status nshb_fp4_dequantize(const nshb_fp4 *Q, const nshb_tensor *X, int32_t n, nshb_stream stream);
+
 /* Synchronises `stream`, then copies the device status word of the last step that used
  * this workspace into *flags (NSHB_DEV_* bits).  The one call that blocks the host. */
 nshb_status nshb_device_status(const void *ws, nshb_stream stream, uint32_t *flags);

@@ -21,7 +21,7 @@ from ._abi import (  # noqa: F401  (re-exported constants)
     NSHB_ERR_UNSUPPORTED, NSHB_DEV_ZERO_NORM_FALLBACK, NSHB_DEV_NONFINITE, NSHB_DEV_TIMEOUT,
     NSHB_DEV_ZERO_RADIUS, NSHB_DEV_NOT_SPD, NSHB_OP_MUON, NSHB_OP_HYPERBALL, NSHB_OP_RADIAL_BRAKE,
     NSHB_OP_HIMUON, NSHB_OP_NEWTON_MUON, NSHB_OP_RELATIVE_UPDATE, NSHB_OP_ADAMH, NSHB_NORM_L2,
-    NSHB_NORM_INF, nshb_matrix, nshb_params, nshb_adam_params, nshb_tensor,
+    NSHB_NORM_INF, NSHB_MXFP4, NSHB_NVFP4, nshb_matrix, nshb_params, nshb_adam_params, nshb_tensor, nshb_fp4,
 )
 
 _LIB = None
@@ -404,6 +404,77 @@ def scale_grads(g, factor, dst=None, stream=None):
 def _same_count(a, b) -> None:
     if b is not None and _n(a) != _n(b):
         raise ValueError(f"{_n(b)} destinations for {_n(a)} tensors")
+
+
+def fp4_size(rows: int, cols: int, format: int) -> tuple:
+    """(bytes of codes, bytes of scales) of a rows x cols 4-bit matrix."""
+    c, s = ctypes.c_size_t(0), ctypes.c_size_t(0)
+    _check(lib().nshb_fp4_size(rows, cols, format, ctypes.byref(c), ctypes.byref(s)), "nshb_fp4_size")
+    return c.value, s.value
+
+
+class Fp4:
+    """A rows x cols matrix in microscaled 4-bit form over the caller's buffers: codes and scales (CUDA
+    uint8, see nshb_fp4 in include/nshb.h for their order) and, for NSHB_NVFP4, the matrix's
+    scale (CUDA float32, one element)."""
+    __slots__ = ("rows", "cols", "format", "codes", "scales", "global_scale", "device")
+
+    def __init__(self, rows: int, cols: int, format: int, codes, scales, global_scale=None):
+        import torch
+        nc, ns = fp4_size(rows, cols, format)
+        _device_arg(codes, "codes", torch.uint8, nc)
+        _device_arg(scales, "scales", torch.uint8, ns)
+        if format == NSHB_NVFP4 and global_scale is None:
+            raise ValueError("NSHB_NVFP4 needs a global_scale")
+        _device_arg(global_scale, "global_scale", torch.float32, 1)
+        if scales.device != codes.device or (global_scale is not None and global_scale.device != codes.device):
+            raise ValueError("codes, scales and global_scale must be on one CUDA device")
+        self.rows, self.cols, self.format = rows, cols, format
+        self.codes, self.scales, self.global_scale = codes, scales, global_scale
+        self.device = codes.device
+
+
+def fp4_empty(rows: int, cols: int, format: int, device=None) -> Fp4:
+    """An Fp4 with buffers of its own, not yet quantised."""
+    import torch
+    nc, ns = fp4_size(rows, cols, format)
+    dev = device or "cuda"
+    return Fp4(rows, cols, format, torch.empty(nc, dtype=torch.uint8, device=dev),
+               torch.empty(ns, dtype=torch.uint8, device=dev),
+               torch.empty(1, dtype=torch.float32, device=dev) if format == NSHB_NVFP4 else None)
+
+
+def fp4_matrices(qs):
+    """ctypes array of nshb_fp4 for a list of Fp4 on one CUDA device (the array keeps them alive)."""
+    arr = (nshb_fp4 * max(len(qs), 1))()
+    dev = qs[0].device if len(qs) else None
+    for i, q in enumerate(qs):
+        if q.device != dev:
+            raise ValueError(f"matrix {i}: every matrix must be on one CUDA device")
+        arr[i].rows, arr[i].cols, arr[i].format = q.rows, q.cols, q.format
+        arr[i].codes, arr[i].scales, arr[i].global_ = _ptr(q.codes), _ptr(q.scales), _ptr(q.global_scale)
+    arr._n = len(qs)
+    arr._keep = (list(qs),)
+    arr._device = dev
+    return arr
+
+
+def fp4_quantize(x, q, ws=None, transpose: bool = False, stream=None):
+    """The 4-bit forms `q` (fp4_matrices) of the tensors `x` (tensors), or of their transposes.  `ws`
+    (tensor_workspace(x)) is needed for NSHB_NVFP4."""
+    if _n(x) != _n(q):
+        raise ValueError(f"{_n(q)} 4-bit matrices for {_n(x)} tensors")
+    ptr, nbytes = (None, 0) if ws is None else _ws(ws)
+    with _On(x, stream, ("q", q), ("workspace", ws)) as st:
+        _check(lib().nshb_fp4_quantize(x, q, _n(x), 1 if transpose else 0, ptr, nbytes, st), "nshb_fp4_quantize")
+
+
+def fp4_dequantize(q, x, stream=None):
+    """The values of the 4-bit matrices `q` into the tensors `x`."""
+    if _n(x) != _n(q):
+        raise ValueError(f"{_n(x)} tensors for {_n(q)} 4-bit matrices")
+    with _On(q, stream, ("x", x)) as st:
+        _check(lib().nshb_fp4_dequantize(q, x, _n(q), st), "nshb_fp4_dequantize")
 
 
 def device_status(ws, stream=None) -> int:

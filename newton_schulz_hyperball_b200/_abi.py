@@ -44,6 +44,9 @@ NSHB_OP_ADAMH = 6
 NSHB_NORM_L2 = 0
 NSHB_NORM_INF = 1
 
+NSHB_MXFP4 = 0
+NSHB_NVFP4 = 1
+
 
 class nshb_matrix(ctypes.Structure):
     _fields_ = [
@@ -101,11 +104,24 @@ class nshb_tensor(ctypes.Structure):
     ]
 
 
+class nshb_fp4(ctypes.Structure):
+    _fields_ = [
+        ("rows", ctypes.c_int64),
+        ("cols", ctypes.c_int64),
+        ("format", ctypes.c_int32),
+        ("reserved", ctypes.c_int32),
+        ("codes", ctypes.c_void_p),
+        ("scales", ctypes.c_void_p),
+        ("global_", ctypes.c_void_p),   # "global" is a Python keyword
+    ]
+
+
 # name -> (restype, argtypes)
 _P = ctypes.c_void_p
 _MATS = ctypes.POINTER(nshb_matrix)
 _PAR = ctypes.POINTER(nshb_params)
 _TENS = ctypes.POINTER(nshb_tensor)
+_FP4 = ctypes.POINTER(nshb_fp4)
 SIGNATURES = {
     "nshb_default_params": (ctypes.c_int32, [_PAR]),
     "nshb_workspace_size": (ctypes.c_int32, [_MATS, ctypes.c_int32, _PAR, ctypes.c_int32,
@@ -134,6 +150,10 @@ SIGNATURES = {
     "nshb_clip_grads": (ctypes.c_int32, [_TENS, _TENS, ctypes.c_int32, ctypes.c_int32, ctypes.c_float, _P, _P,
                                          ctypes.c_size_t, _P]),
     "nshb_scale_grads": (ctypes.c_int32, [_TENS, _TENS, ctypes.c_int32, _P, _P]),
+    "nshb_fp4_size": (ctypes.c_int32, [ctypes.c_int64, ctypes.c_int64, ctypes.c_int32,
+                                       ctypes.POINTER(ctypes.c_size_t), ctypes.POINTER(ctypes.c_size_t)]),
+    "nshb_fp4_quantize": (ctypes.c_int32, [_TENS, _FP4, ctypes.c_int32, ctypes.c_int32, _P, ctypes.c_size_t, _P]),
+    "nshb_fp4_dequantize": (ctypes.c_int32, [_FP4, _TENS, ctypes.c_int32, _P]),
     "nshb_device_status": (ctypes.c_int32, [_P, _P, ctypes.POINTER(ctypes.c_uint32)]),
     "nshb_status_string": (ctypes.c_char_p, [ctypes.c_int32]),
     "nshb_version": (ctypes.c_int32, []),

@@ -398,6 +398,28 @@ __host__ __device__ inline int win_cta(int w, int nwin, int nctas) {
   return (int)((((int64_t)w + 1) * nctas - 1) / nwin);
 }
 
+// Microscaled 4-bit matrices (fp4.cu), in tiles of 128 rows x 128 columns of the 4-bit matrix.
+constexpr int kMaxFp4 = 224;
+constexpr int kFp4F32 = 1;      // the other side (source, or values) is fp32 (else bf16)
+constexpr int kFp4Nv = 2;       // NSHB_NVFP4 (else NSHB_MXFP4)
+constexpr int kFp4Vec = 4;      // the other side's rows may be accessed 16 bytes at a time
+struct Fp4Item {
+  void *x;                 // source of a quantisation, destination of the values
+  uint8_t *codes, *scales;
+  float *global;
+  int64_t ld;              // of x
+  int32_t rows, cols;      // of the 4-bit matrix
+  int32_t ktiles;          // round_up(cols, 128) / 128
+  int32_t tile_begin;
+  int32_t flags;
+  int32_t rec_begin, n_rec;   // kFp4Nv: records of the source's largest magnitude
+};
+struct Fp4Params {
+  const double *rec;
+  int32_t n, total_tiles;
+  Fp4Item item[kMaxFp4];
+};
+
 // Launchers (defined in the .cu files); each returns cudaGetLastError().
 cudaError_t launch_momentum(const MomentumParams &p, cudaStream_t s);
 cudaError_t launch_norm_finalize(const NormFinParams &p, int nseg_total, cudaStream_t s);
@@ -428,6 +450,8 @@ cudaError_t launch_potrf_diag(const DiagParams &p, cudaStream_t s);
 cudaError_t launch_tens_norm(const TensParams &p, cudaStream_t s);
 cudaError_t launch_tens_finalize(const TensFinParams &p, cudaStream_t s);
 cudaError_t launch_tens_scale(const TensParams &p, cudaStream_t s);
+cudaError_t launch_fp4_quantize(const Fp4Params &p, bool transpose, cudaStream_t s);
+cudaError_t launch_fp4_dequantize(const Fp4Params &p, cudaStream_t s);
 
 constexpr size_t kMaxParamBytes = 32764;   // kernel parameter limit (CUDA 12.1+, sm_70+)
 static_assert(sizeof(MomentumParams) <= kMaxParamBytes, "MomentumParams");
@@ -442,6 +466,7 @@ static_assert(sizeof(SyrkParams) <= kMaxParamBytes, "SyrkParams");
 static_assert(sizeof(CholParams) <= kMaxParamBytes, "CholParams");
 static_assert(sizeof(NwParams) <= kMaxParamBytes, "NwParams");
 static_assert(sizeof(SplitParams) <= kMaxParamBytes, "SplitParams");
+static_assert(sizeof(Fp4Params) <= kMaxParamBytes, "Fp4Params");
 static_assert(sizeof(TensParams) <= kMaxParamBytes, "TensParams");
 static_assert(sizeof(TensFinParams) <= kMaxParamBytes, "TensFinParams");
 static_assert(sizeof(DiagParams) <= kMaxParamBytes, "DiagParams");

@@ -185,6 +185,30 @@ nshb_status run_scale(const nshb_tensor *src, const nshb_tensor *dst, int32_t n,
   return NSHB_OK;
 }
 
+}  // namespace
+
+nshb_status run_largest(const nshb_tensor *t, int32_t n, const TensWorkspace &w, cudaStream_t st, int32_t *rec_begin,
+                        int32_t *n_rec) {
+  int32_t i = 0;
+  TensParams p;
+  std::memset(&p, 0, offsetof(TensParams, t));
+  const nshb_status e = fill_launch(t, nullptr, n, i, p, nullptr);
+  if (e != NSHB_OK) return e;
+  if (i != n) return NSHB_ERR_UNSUPPORTED;
+  p.rec = w.rec;
+  p.kind = kNormFinite;
+  for (int k = 0; k < p.ntens; ++k) {
+    const int end = k + 1 < p.ntens ? p.t[k + 1].win_begin : p.nwin;
+    const int c0 = win_cta(p.t[k].win_begin, p.nwin, p.nctas), c1 = win_cta(end - 1, p.nwin, p.nctas);
+    rec_begin[k] = c0 + k;
+    n_rec[k] = c1 - c0 + 1;
+  }
+  NSHB_RUN(NSHB_PROF_FP4, launch_tens_norm(p, st));
+  return NSHB_OK;
+}
+
+namespace {
+
 nshb_status check_norm_args(const nshb_tensor *g, int32_t n, int32_t kind, float max_norm, const float *total) {
   const nshb_status e = check_tensors(g, n);
   if (e != NSHB_OK) return e;

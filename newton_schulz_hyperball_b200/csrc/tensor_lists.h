@@ -33,5 +33,11 @@ nshb_status check_tens_ws(void *ws, size_t bytes, int32_t n);
 nshb_status check_tensor(const nshb_tensor &t);
 nshb_status check_tensors(const nshb_tensor *t, int32_t n);
 int tens_ctas(int nwin, int per_sm);
+// The largest finite magnitude of each of up to kMaxTens tensors with elements, left as records: tensor k's
+// are w.rec[rec_begin[k]] .. [+ n_rec[k]), each the bits of a magnitude as a double.
+nshb_status run_largest(const nshb_tensor *t, int32_t n, const TensWorkspace &w, cudaStream_t st, int32_t *rec_begin,
+                        int32_t *n_rec);
+constexpr int64_t kMaxFp4Dim = 1LL << 24;
+nshb_status check_fp4(const nshb_fp4 &q);
 
 }  // namespace nshb

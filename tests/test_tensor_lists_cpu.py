@@ -98,3 +98,70 @@ def test_the_binding_refuses_what_the_library_cannot_see():
         nshb.grad_norm(t, torch.zeros(2), (WS, 1 << 20))
     with pytest.raises(ValueError, match="2 destinations for 1"):
         nshb.clip_grads(t, 1.0, TOTAL, (WS, 1 << 20), dst=fake((3, 5), (3, 5)))
+
+
+# ------------------------------------------------------------------- 4-bit matrices
+
+
+def fake4(*shapes, fmt=nshb.NSHB_NVFP4):
+    arr = (nshb.nshb_fp4 * max(len(shapes), 1))()
+    for i, (r, c) in enumerate(shapes):
+        arr[i].rows, arr[i].cols, arr[i].format = r, c, fmt
+        arr[i].codes, arr[i].scales, arr[i].global_ = 0x40000000 + 0x1000000 * i, 0x50000000 + 0x1000000 * i, 0x60000000
+    arr._n = len(shapes)
+    return arr
+
+
+def quantize(x, q, transpose=0, ws=WS, ws_bytes=1 << 20, n=None):
+    return nshb.lib().nshb_fp4_quantize(x, q, q._n if n is None else n, transpose, ws, ws_bytes, None)
+
+
+def dequantize(q, x):
+    return nshb.lib().nshb_fp4_dequantize(q, x, q._n, None)
+
+
+def test_fp4_layout_and_sizes():
+    assert ctypes.sizeof(nshb.nshb_fp4) == 48
+    assert nshb.fp4_size(1, 1, nshb.NSHB_MXFP4) == (64, 512)
+    assert nshb.fp4_size(129, 129, nshb.NSHB_MXFP4) == (129 * 128, 256 * 8)
+    assert nshb.fp4_size(129, 129, nshb.NSHB_NVFP4) == (129 * 128, 256 * 16)
+    assert nshb.fp4_size(0, 7, nshb.NSHB_MXFP4) == (0, 0)
+    for args, code in (((-1, 1, 0), nshb.NSHB_ERR_SHAPE), ((1, -1, 0), nshb.NSHB_ERR_SHAPE), ((1, 1, 2), nshb.NSHB_ERR_DTYPE),
+                       (((1 << 24) + 1, 1, 0), nshb.NSHB_ERR_UNSUPPORTED)):
+        with pytest.raises(nshb.NshbError) as e:
+            nshb.fp4_size(*args)
+        assert e.value.status == code
+
+
+@pytest.mark.parametrize("change,code", [
+    (dict(rows=-1), nshb.NSHB_ERR_SHAPE),
+    (dict(rows=3), nshb.NSHB_ERR_SHAPE),
+    (dict(cols=6), nshb.NSHB_ERR_SHAPE),
+    (dict(cols=(1 << 24) + 1), nshb.NSHB_ERR_UNSUPPORTED),
+    (dict(format=2), nshb.NSHB_ERR_DTYPE),
+    (dict(reserved=5), nshb.NSHB_ERR_PARAM),
+    (dict(codes=None), nshb.NSHB_ERR_NULL),
+    (dict(scales=None), nshb.NSHB_ERR_NULL),
+    (dict(global_=None), nshb.NSHB_ERR_NULL),
+    (dict(codes=0x40000008), nshb.NSHB_ERR_SHAPE),
+    (dict(scales=0x50000004), nshb.NSHB_ERR_SHAPE),
+    (dict(global_=0x60000002), nshb.NSHB_ERR_SHAPE),
+])
+def test_a_bad_4_bit_matrix_is_refused(change, code):
+    x, q = fake((4, 5), (2, 5)), fake4((4, 5), (2, 5))
+    for k, v in change.items():
+        setattr(q[1], k, v)
+    assert quantize(x, q) == dequantize(q, x) == code
+
+
+def test_bad_quantize_arguments():
+    x, q = fake((4, 5)), fake4((4, 5))
+    assert quantize(x, q, transpose=1) == nshb.NSHB_ERR_SHAPE
+    assert quantize(x, q, n=-1) == nshb.NSHB_ERR_SHAPE
+    assert quantize(x, q, ws=None) == nshb.NSHB_ERR_NULL
+    assert quantize(x, q, ws_bytes=64) == quantize(x, q, ws=WS + 64) == nshb.NSHB_ERR_WORKSPACE
+    assert nshb.lib().nshb_fp4_quantize(x, None, 1, 0, WS, 1 << 20, None) == nshb.NSHB_ERR_NULL
+    x[0].dtype = 3
+    assert quantize(x, q) == dequantize(q, x) == nshb.NSHB_ERR_DTYPE
+    with pytest.raises(ValueError, match="1 4-bit matrices for 2"):
+        nshb.fp4_quantize(fake((4, 5), (4, 5)), q)
