@@ -343,6 +343,17 @@ nshb_status nshb_fp4_quantize(const nshb_tensor *X, const nshb_fp4 *Q, int32_t n
 /* X[i] = the values of Q[i] (same rows and cols), rounded once to X[i]'s dtype. */
 nshb_status nshb_fp4_dequantize(const nshb_fp4 *Q, const nshb_tensor *X, int32_t n, nshb_stream stream);
 
+/* D[i] = A[i] B[i]^T (rows of A x rows of B, bf16 or fp32, any ld), or with B == NULL the Gram matrix
+ * A[i] A[i]^T (both triangles): products of 4-bit matrices of one format and equal cols on the tensor
+ * cores, fp32 accumulation, multiplied by both global scales and rounded once.  cols == 0 gives
+ * zeros.  A NaN scale makes the rows (columns) of D that use it NaN.  D must not overlap the
+ * operands.  The tensor cores read the operands in place.  Any sizes from one row (a single token) on;
+ * the number of CTAs that share a sum, and so its order, depends on the sizes and on nothing else.
+ * ws: nshb_tensor_workspace_size(D, n) bytes; its status word is cleared first and gets
+ * NSHB_DEV_TIMEOUT if a bounded wait ran out. */
+nshb_status nshb_fp4_matmul(const nshb_fp4 *A, const nshb_fp4 *B, const nshb_tensor *D, int32_t n, void *ws,
+                            size_t ws_bytes, nshb_stream stream);
+
 /* Synchronises `stream`, then copies the device status word of the last step that used
  * this workspace into *flags (NSHB_DEV_* bits).  The one call that blocks the host. */
 nshb_status nshb_device_status(const void *ws, nshb_stream stream, uint32_t *flags);

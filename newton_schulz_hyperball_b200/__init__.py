@@ -477,6 +477,16 @@ def fp4_dequantize(q, x, stream=None):
         _check(lib().nshb_fp4_dequantize(q, x, _n(q), st), "nshb_fp4_dequantize")
 
 
+def fp4_matmul(a, b, d, ws, stream=None):
+    """d[i] = a[i] b[i]^T of the 4-bit matrices `a` and `b` into the tensors `d`; with b None the Gram
+    matrices a[i] a[i]^T.  `ws`: tensor_workspace(d)."""
+    if _n(a) != _n(d) or (b is not None and _n(b) != _n(d)):
+        raise ValueError(f"{_n(a)} and {_n(b) if b is not None else _n(a)} operands for {_n(d)} results")
+    ptr, nbytes = _ws(ws)
+    with _On(d, stream, ("a", a), ("b", b), ("workspace", ws)) as st:
+        _check(lib().nshb_fp4_matmul(a, b, d, _n(d), ptr, nbytes, st), "nshb_fp4_matmul")
+
+
 def device_status(ws, stream=None) -> int:
     ptr, _ = _ws(ws)
     v = ctypes.c_uint32(0)

@@ -154,6 +154,7 @@ SIGNATURES = {
                                        ctypes.POINTER(ctypes.c_size_t), ctypes.POINTER(ctypes.c_size_t)]),
     "nshb_fp4_quantize": (ctypes.c_int32, [_TENS, _FP4, ctypes.c_int32, ctypes.c_int32, _P, ctypes.c_size_t, _P]),
     "nshb_fp4_dequantize": (ctypes.c_int32, [_FP4, _TENS, ctypes.c_int32, _P]),
+    "nshb_fp4_matmul": (ctypes.c_int32, [_FP4, _FP4, _TENS, ctypes.c_int32, _P, ctypes.c_size_t, _P]),
     "nshb_device_status": (ctypes.c_int32, [_P, _P, ctypes.POINTER(ctypes.c_uint32)]),
     "nshb_status_string": (ctypes.c_char_p, [ctypes.c_int32]),
     "nshb_version": (ctypes.c_int32, []),

@@ -15,7 +15,7 @@ CSRC = os.path.join(PKG, "csrc")
 LIB = os.path.join(PKG, "libnshb.so")
 SOURCES = ["api.cu", "stream_kernels.cu", "ns_f32.cu", "ns_tc2.cu", "himuon_tile.cu", "newton.cu", "newton_tc.cu",
            "norms_static.cu", "grad_norm.cu", "tensor_api.cu",
-           "fp4.cu", "fp4_api.cu"]
+           "fp4.cu", "fp4_gemm.cu", "fp4_api.cu"]
 HEADERS = ["nshb_internal.h", "nshb_device.cuh", "tensor_lists.h"]
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 

@@ -57,7 +57,106 @@ nshb_status check_pairs(const nshb_tensor *x, const nshb_fp4 *q, int32_t n, bool
   return NSHB_OK;
 }
 
+// How one product is laid over the GPU.
+struct Shape {
+  int bn, split;
+  bool swap;      // the caller's B takes the accumulator's lanes
+  int64_t tiles;
+};
+
+Shape shape_of(int64_t m, int64_t n, int64_t kt, bool sym) {
+  Shape s = {128, 1, false, 0};
+  int64_t p = m, q = n;
+  if (!sym && std::min(m, n) <= 64) {
+    s.swap = m < n;
+    if (s.swap) std::swap(p, q);
+    s.bn = q <= 16 ? 16 : q <= 32 ? 32 : 64;
+  }
+  const int64_t pt = (p + 127) / 128, qt = (q + s.bn - 1) / s.bn;
+  s.tiles = sym ? pt * (pt + 1) / 2 : pt * qt;
+  while (s.split < 8 && s.split * 2 <= kt && s.tiles * s.split * 2 <= 2 * device_sms()) s.split *= 2;
+  return s;
+}
+
+nshb_status check_products(const nshb_fp4 *A, const nshb_fp4 *B, const nshb_tensor *D, int32_t n) {
+  const nshb_status e = check_tensors(D, n);
+  if (e != NSHB_OK) return e;
+  if (n > 0 && !A) return NSHB_ERR_NULL;
+  for (int32_t i = 0; i < n; ++i) {
+    const nshb_fp4 &a = A[i], &b = B ? B[i] : A[i];
+    nshb_status ce = check_fp4(a);
+    if (ce == NSHB_OK) ce = check_fp4(b);
+    if (ce != NSHB_OK) return ce;
+    if (a.format != b.format) return NSHB_ERR_DTYPE;
+    if (a.cols != b.cols || D[i].rows != a.rows || D[i].cols != b.rows) return NSHB_ERR_SHAPE;
+  }
+  return NSHB_OK;
+}
+
 }  // namespace
+
+// Products of one launch; `d` as the caller stores it.  See launch_fp4_gemm for what the launches share.
+nshb_status run_fp4_products(const nshb_fp4 *A, const nshb_fp4 *B, const nshb_tensor *D, int32_t n, uint32_t *status,
+                             bool clear, long long limit, cudaStream_t st) {
+  int32_t i = 0;
+  while (i < n) {
+    Fp4GemmParams p;
+    std::memset(&p, 0, offsetof(Fp4GemmParams, prob));
+    p.status = status;
+    p.wait_limit = limit;
+    p.clear_status = clear;
+    Shape first = {0, 0, false, 0};
+    int32_t format = 0;
+    int64_t tiles = 0;
+    for (; i < n && p.nprob < kMaxFp4Prob; ++i) {
+      const nshb_fp4 &a = A[i], &b = B ? B[i] : A[i];
+      if (D[i].rows == 0 || D[i].cols == 0) continue;
+      const int64_t kt = (a.cols + 255) / 256;
+      const bool sym = !B;
+      const Shape s = shape_of(D[i].rows, D[i].cols, kt, sym);
+      if (p.nprob && (s.bn != first.bn || s.split != first.split || a.format != format)) break;
+      if ((tiles + s.tiles) * s.split > (1LL << 30)) {
+        if (p.nprob) break;
+        return NSHB_ERR_UNSUPPORTED;
+      }
+      first = s;
+      format = a.format;
+      Fp4Prob &q = p.prob[p.nprob++];
+      std::memset(&q, 0, sizeof(q));
+      const nshb_fp4 &P = s.swap ? b : a, &Q = s.swap ? a : b;
+      if (kt) {
+        cudaError_t e = encode_fp4_maps(&q.pc, &q.ps, P, 128, 1);
+        if (e == cudaSuccess) e = encode_fp4_maps(&q.qc, &q.qs, Q, s.bn, 1);
+        if (e != cudaSuccess) {
+          record_cuda_error(e);
+          return NSHB_ERR_CUDA;
+        }
+        if (a.format == NSHB_NVFP4) {
+          q.pg = P.global;
+          q.qg = Q.global;
+        }
+      }
+      const bool f32 = D[i].dtype == NSHB_F32;
+      q.d = D[i].data;
+      q.ld = D[i].rows == 1 ? D[i].cols : D[i].ld;
+      q.np = (int32_t)(s.swap ? D[i].cols : D[i].rows);
+      q.nq = (int32_t)(s.swap ? D[i].rows : D[i].cols);
+      q.kt = (int32_t)kt;
+      q.qtiles = (q.nq + s.bn - 1) / s.bn;
+      q.tile_begin = (int32_t)tiles;
+      const bool vec = (uintptr_t)D[i].data % 16 == 0 && (D[i].rows == 1 || (q.ld * (f32 ? 4 : 2)) % 16 == 0);
+      q.flags = (s.swap ? kFp4DTrans : 0) | (f32 ? kFp4DF32 : 0) | (sym ? kFp4Sym : 0) | (vec ? kFp4DVec : 0);
+      tiles += s.tiles;
+    }
+    if (!p.nprob) break;
+    p.total_tiles = (int32_t)tiles;
+    NSHB_RUN(NSHB_PROF_FP4, launch_fp4_gemm(p, first.bn, first.split, format == NSHB_NVFP4, st));
+    clear = false;
+  }
+  if (clear) NSHB_RUN(NSHB_PROF_FP4, cudaMemsetAsync(status, 0, sizeof(uint32_t), st));
+  return NSHB_OK;
+}
+
 }  // namespace nshb
 
 using namespace nshb;
@@ -138,6 +237,15 @@ nshb_status nshb_fp4_dequantize(const nshb_fp4 *Q, const nshb_tensor *X, int32_t
     NSHB_RUN(NSHB_PROF_FP4, launch_fp4_dequantize(p, st));
   }
   return NSHB_OK;
+}
+
+nshb_status nshb_fp4_matmul(const nshb_fp4 *A, const nshb_fp4 *B, const nshb_tensor *D, int32_t n, void *ws,
+                            size_t ws_bytes, nshb_stream stream) {
+  nshb_status e = check_products(A, B, D, n);
+  if (e != NSHB_OK) return e;
+  e = check_tens_ws(ws, ws_bytes, n);
+  if (e != NSHB_OK) return e;
+  return run_fp4_products(A, B, D, n, static_cast<uint32_t *>(ws), /*clear=*/true, kFp4WaitLimit, (cudaStream_t)stream);
 }
 
 }  // extern "C"

@@ -1,0 +1,366 @@
+// Products of microscaled 4-bit matrices on the 5th-generation tensor cores:
+//
+//   D = gP gQ  sum_k (code_P scale_P)(code_Q scale_Q)      (tcgen05.mma kind::mxf4nvf4, fp32 accumulator)
+//
+// The codes go from memory to the tensor core as they are stored: one 128-byte box holds 256
+// columns of a row.  The scales of a step (512-byte tiles, see nshb_fp4) are loaded next to the
+// codes and copied into tensor memory by tcgen05.cp, which the same thread issues ahead of the MMAs that
+// read them (the two run in order).
+//
+// One CTA computes 128 rows of P x BN rows of Q.  Few rows on one side (single tokens) are bound by
+// the bytes of the other operand: that one takes the 128 lanes, BN is as small as the rows allow,
+// and a cluster of up to 8 CTAs shares the columns of one tile, each summing its part; the parts are joined
+// through distributed shared memory in a fixed order.
+//
+// Roles (192 threads): warp 0 issues the loads of the ring, warp 1 the copies and MMAs, warps
+// 2-5 drain the accumulator.  Every wait is bounded.
+#include <cuda.h>
+#include <cuda_runtime.h>
+#include <cuda_bf16.h>
+
+#include <type_traits>
+
+#include "nshb_device.cuh"
+#include "nshb_internal.h"
+
+namespace nshb {
+namespace {
+
+constexpr int kThreads = 192;
+constexpr uint32_t kTimeoutBit = 0x4u;
+
+template <int BN, bool NV>
+struct Cfg {
+  static constexpr int kSTiles = NV ? 4 : 2;                 // 512-byte scale tiles of a step and 128 rows
+  static constexpr int kQRowTiles = BN > 128 ? 2 : 1;
+  static constexpr int kPBytes = 128 * 128, kQBytes = BN * 128;
+  static constexpr int kPs = kSTiles * 512, kQs = kSTiles * 512 * kQRowTiles;
+  static constexpr int kStage = kPBytes + kQBytes + kPs + kQs;   // a multiple of 1024
+  // two CTAs on an SM up to BN = 128
+  static constexpr int kStages = BN > 128 ? 4 : 110 * 1024 / kStage;
+  static constexpr int kSmem = kStages * kStage + 1024 + 256;
+  static constexpr int kPsCol = BN < 32 ? 32 : BN;           // TMEM columns: accumulator, P's scales, Q's
+  static constexpr int kQsCol = kPsCol + 4 * kSTiles;
+  static constexpr int kUsed = kQsCol + 4 * kSTiles * kQRowTiles;
+  static constexpr int kTmem = kUsed <= 64 ? 64 : kUsed <= 128 ? 128 : kUsed <= 256 ? 256 : 512;
+  static_assert(kStage % 1024 == 0, "every stage starts on a swizzle atom");
+  static_assert(128 * BN * 4 <= kStages * kStage, "the partial sums fit the ring");
+};
+
+__device__ __forceinline__ int find_prob(const Fp4GemmParams &p, int tile) {
+  int lo = 0, hi = p.nprob - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (p.prob[mid].tile_begin <= tile) lo = mid; else hi = mid - 1;
+  }
+  return lo;
+}
+
+// Tile l of a problem: its P and Q tile (all, or those on and below the diagonal).
+__device__ __forceinline__ void tile_of(const Fp4Prob &q, int l, int &pt, int &qt) {
+  if (q.flags & kFp4Sym) {
+    pt = (int)((sqrtf(8.f * (float)l + 1.f) - 1.f) * 0.5f);
+    while (pt * (pt + 1) / 2 > l) --pt;
+    while ((pt + 1) * (pt + 2) / 2 <= l) ++pt;
+    qt = l - pt * (pt + 1) / 2;
+  } else {
+    pt = l / q.qtiles;
+    qt = l - pt * q.qtiles;
+  }
+}
+
+// N values of D: row p, columns q0 .. q0 + N - 1 of the tile's orientation.
+template <int N>
+__device__ __forceinline__ void store_row(const Fp4Prob &q, int64_t p, int64_t q0, const float (&v)[N], bool trans) {
+  if (p >= q.np) return;
+  const bool f32 = q.flags & kFp4DF32;
+  if (trans) {
+#pragma unroll
+    for (int e = 0; e < N; ++e) {
+      if (q0 + e >= q.nq) break;
+      const int64_t at = (q0 + e) * q.ld + p;
+      if (f32) static_cast<float *>(q.d)[at] = v[e];
+      else static_cast<__nv_bfloat16 *>(q.d)[at] = __float2bfloat16_rn(v[e]);
+    }
+    return;
+  }
+  const int64_t at = p * q.ld + q0;
+  if (N >= 8 && (q.flags & kFp4DVec) && q0 + N <= q.nq) {
+    if (f32) {
+      float4 *d = reinterpret_cast<float4 *>(static_cast<float *>(q.d) + at);
+#pragma unroll
+      for (int e = 0; e < N / 4; ++e) d[e] = make_float4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
+    } else {
+      uint4 *d = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(q.d) + at);
+#pragma unroll
+      for (int e = 0; e < N / 8; ++e)
+        d[e] = make_uint4(pack_bf16(v[8 * e], v[8 * e + 1]), pack_bf16(v[8 * e + 2], v[8 * e + 3]),
+                          pack_bf16(v[8 * e + 4], v[8 * e + 5]), pack_bf16(v[8 * e + 6], v[8 * e + 7]));
+    }
+    return;
+  }
+#pragma unroll
+  for (int e = 0; e < N; ++e) {
+    if (q0 + e >= q.nq) break;
+    if (f32) static_cast<float *>(q.d)[at + e] = v[e];
+    else static_cast<__nv_bfloat16 *>(q.d)[at + e] = __float2bfloat16_rn(v[e]);
+  }
+}
+
+template <int BN, bool NV, bool SPLIT>
+__global__ void __launch_bounds__(kThreads, BN > 128 ? 1 : 2) fp4_gemm_kernel(const __grid_constant__ Fp4GemmParams p) {
+  using C = Cfg<BN, NV>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint64_t *bars = reinterpret_cast<uint64_t *>(smem + C::kStages * C::kStage);
+  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + 2 * C::kStages + 1);
+  const uint32_t base = smem_u32(smem), bar_base = smem_u32(bars);
+  auto full = [&](int s) { return bar_base + 8u * s; };
+  auto empty = [&](int s) { return bar_base + 8u * (C::kStages + s); };
+  const uint32_t done = bar_base + 8u * (2 * C::kStages);
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int part = SPLIT ? (int)cta_rank() : 0;
+  int parts = 1;
+  if (SPLIT) asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(parts));
+  const int tile = (int)blockIdx.x / parts;
+  const Fp4Prob &q = p.prob[find_prob(p, tile)];
+  int pt, qt;
+  tile_of(q, tile - q.tile_begin, pt, qt);
+  const int k0 = (int)((int64_t)part * q.kt / parts), k1 = (int)((int64_t)(part + 1) * q.kt / parts);
+  const long long limit = p.wait_limit;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < C::kStages; ++s) {
+      mbar_init(full(s), 1);
+      mbar_init(empty(s), 1);
+    }
+    mbar_init(done, 1);
+    mbar_fence_init();
+    if (q.kt) {
+      prefetch_tmap(&q.pc);
+      prefetch_tmap(&q.qc);
+      prefetch_tmap(&q.ps);
+      prefetch_tmap(&q.qs);
+    }
+  }
+  if (warp == 1) {
+    tmem_alloc(smem_u32(tmem_slot), C::kTmem);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  pdl_trigger();
+  pdl_wait();
+  // No wait can run out before this: the shortest limit is about a millisecond.
+  if (p.clear_status && blockIdx.x == 0 && threadIdx.x == 0) *p.status = 0;
+
+  if (warp == 0) {
+    if (lane == 0) {
+      int stage = 0;
+      uint32_t phase = 0;
+      int last_parity[C::kStages];
+#pragma unroll
+      for (int s = 0; s < C::kStages; ++s) last_parity[s] = -1;
+      for (int kb = k0; kb < k1; ++kb) {
+        if (!mbar_wait(empty(stage), phase ^ 1u, limit)) {
+          set_status(p.status, kTimeoutBit);
+          break;
+        }
+        const uint32_t sp = base + stage * C::kStage, sq = sp + C::kPBytes, ss = sq + C::kQBytes;
+        mbar_arrive_expect_tx(full(stage), C::kStage);
+#pragma unroll
+        for (int s = 0; s < C::kStages; ++s)
+          if (s == stage) last_parity[s] = (int)phase;
+        tma_load_2d(sp, &q.pc, kb * 128, pt * 128, full(stage));
+        tma_load_2d(sq, &q.qc, kb * 128, qt * BN, full(stage));
+        tma_load_3d(ss, &q.ps, 0, kb * C::kSTiles, pt, full(stage));
+        tma_load_3d(ss + C::kPs, &q.qs, 0, kb * C::kSTiles, qt * C::kQRowTiles, full(stage));
+        if (++stage == C::kStages) {
+          stage = 0;
+          phase ^= 1u;
+        }
+      }
+      // every load that was started must have landed before this CTA leaves
+#pragma unroll
+      for (int s = 0; s < C::kStages; ++s)
+        if (last_parity[s] >= 0 && !mbar_wait(full(s), (uint32_t)last_parity[s], limit)) set_status(p.status, kTimeoutBit);
+    }
+  } else if (warp == 1) {
+    if (lane == 0) {
+      int stage = 0;
+      uint32_t phase = 0;
+      bool ok = true;
+      for (int kb = k0; kb < k1; ++kb) {
+        if (!mbar_wait(full(stage), phase, limit)) {
+          set_status(p.status, kTimeoutBit);
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        const uint32_t sp = base + stage * C::kStage, sq = sp + C::kPBytes, ss = sq + C::kQBytes;
+#pragma unroll
+        for (int j = 0; j < C::kSTiles; ++j) {
+          tc_cp_scales(tmem + C::kPsCol + 4 * j, smem_desc_scales(ss + 512 * j));
+#pragma unroll
+          for (int i = 0; i < C::kQRowTiles; ++i)
+            tc_cp_scales(tmem + C::kQsCol + 4 * (C::kQRowTiles * j + i),
+                         smem_desc_scales(ss + C::kPs + 512 * (C::kSTiles * i + j)));
+        }
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          // 64 columns: 32 bytes inside the swizzled rows; MX: half of a scale word, NV: a whole one
+          const int j = NV ? k : k >> 1, id = NV ? 0 : 2 * (k & 1);
+          tc_mma_fp4<NV>(tmem, smem_desc_sw128(sp + 32 * k, 16, 1024), smem_desc_sw128(sq + 32 * k, 16, 1024),
+                         idesc_fp4(128, BN, NV, id), tmem + C::kPsCol + 4 * j, tmem + C::kQsCol + 4 * C::kQRowTiles * j,
+                         kb != k0 || k != 0);
+        }
+        tc_commit(empty(stage));
+        if (++stage == C::kStages) {
+          stage = 0;
+          phase ^= 1u;
+        }
+      }
+      if (ok && k1 > k0) tc_commit(done);
+    }
+  }
+  // Warps 2-5: lanes 32 (warp mod 4) .. + 31 of the accumulator.  The rest waits for them below.
+  const int quarter = warp & 3;
+  const int row = quarter * 32 + lane;
+  const bool epi = warp >= 2;
+  bool have = k1 > k0;
+  const float g = q.pg ? *q.pg * *q.qg : 1.f;
+  const bool trans = q.flags & kFp4DTrans, sym = q.flags & kFp4Sym;
+  constexpr int N = BN < 32 ? BN : 32;
+  if (epi && have && !mbar_wait(done, 0, limit)) {
+    set_status(p.status, kTimeoutBit);
+    have = false;
+  }
+  __syncwarp();
+  tc_fence_after();
+  auto read = [&](int c, float (&v)[N]) {
+    uint32_t r[N];
+    if constexpr (N == 16) tmem_ld16(tmem + c + ((uint32_t)(quarter * 32) << 16), r);
+    else tmem_ld32(tmem + c + ((uint32_t)(quarter * 32) << 16), r);
+    tmem_ld_wait();
+#pragma unroll
+    for (int e = 0; e < N; ++e) v[e] = __uint_as_float(r[e]);
+  };
+  auto store = [&](int c, float (&v)[N]) {
+#pragma unroll
+    for (int e = 0; e < N; ++e) v[e] *= g;
+    store_row<N>(q, (int64_t)pt * 128 + row, (int64_t)qt * BN + c, v, trans);
+    if (sym && pt != qt) store_row<N>(q, (int64_t)pt * 128 + row, (int64_t)qt * BN + c, v, true);
+  };
+  if (!SPLIT) {
+    if (epi) {
+#pragma unroll 1
+      for (int c = 0; c < BN; c += N) {
+        float v[N];
+        if (have) read(c, v);
+        else {
+#pragma unroll
+          for (int e = 0; e < N; ++e) v[e] = 0.f;
+        }
+        store(c, v);
+      }
+    }
+  } else {
+    // The parts: column by column into this CTA's ring, which its own MMAs have left, then every CTA
+    // sums the columns that fall to it, part 0 first.
+    float *mine = reinterpret_cast<float *>(smem);
+    if (epi) {
+#pragma unroll 1
+      for (int c = 0; c < BN; c += N) {
+        float v[N];
+        if (have) read(c, v);
+#pragma unroll
+        for (int e = 0; e < N; ++e) mine[(c + e) * 128 + row] = have ? v[e] : 0.f;
+      }
+    }
+    cluster_sync();
+    if (epi) {
+      // BN and parts are powers of two: a CTA takes 2 columns or more
+      auto join = [&](int c, auto width) {
+        constexpr int W = decltype(width)::value;
+        float v[W];
+#pragma unroll
+        for (int e = 0; e < W; ++e) v[e] = 0.f;
+        for (int r = 0; r < parts; ++r) {
+          const uint32_t from = mapa(base + (uint32_t)((c * 128 + row) * 4), (uint32_t)r);
+#pragma unroll
+          for (int e = 0; e < W; ++e) v[e] += ld_cluster(from + 512u * e);
+        }
+#pragma unroll
+        for (int e = 0; e < W; ++e) v[e] *= g;
+        store_row<W>(q, (int64_t)pt * 128 + row, (int64_t)qt * BN + c, v, trans);
+        if (sym && pt != qt) store_row<W>(q, (int64_t)pt * 128 + row, (int64_t)qt * BN + c, v, true);
+      };
+      const int each = BN / parts, c0 = each * part;
+      if (each >= 8) {
+        for (int c = c0; c < c0 + each; c += 8) join(c, std::integral_constant<int, 8>());
+      } else {
+        for (int c = c0; c < c0 + each; c += 2) join(c, std::integral_constant<int, 2>());
+      }
+    }
+    cluster_sync();   // no CTA leaves while another may still read its shared memory
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, C::kTmem);
+  }
+}
+
+template <int BN, bool NV, bool SPLIT>
+cudaError_t launch(const Fp4GemmParams &p, int split, cudaStream_t s) {
+  using C = Cfg<BN, NV>;
+  static PerDevice attr_set;
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (!attr_set.get(dev)) {
+    e = cudaFuncSetAttribute(fp4_gemm_kernel<BN, NV, SPLIT>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+    if (e != cudaSuccess) return e;
+    attr_set.set(dev, 1);
+  }
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(p.total_tiles * split, 1, 1);
+  cfg.blockDim = dim3(kThreads, 1, 1);
+  cfg.dynamicSmemBytes = C::kSmem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = split;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = SPLIT ? 2 : 1;
+  e = cudaLaunchKernelEx(&cfg, fp4_gemm_kernel<BN, NV, SPLIT>, p);
+  return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+template <int BN, bool NV>
+cudaError_t launch_bn(const Fp4GemmParams &p, int split, cudaStream_t s) {
+  return split > 1 ? launch<BN, NV, true>(p, split, s) : launch<BN, NV, false>(p, 1, s);
+}
+
+}  // namespace
+
+cudaError_t launch_fp4_gemm(const Fp4GemmParams &p, int bn, int split, bool nv, cudaStream_t s) {
+  if (p.total_tiles <= 0) return cudaSuccess;
+  switch (bn) {
+    case 16: return nv ? launch_bn<16, true>(p, split, s) : launch_bn<16, false>(p, split, s);
+    case 32: return nv ? launch_bn<32, true>(p, split, s) : launch_bn<32, false>(p, split, s);
+    case 64: return nv ? launch_bn<64, true>(p, split, s) : launch_bn<64, false>(p, split, s);
+    case 128: return nv ? launch_bn<128, true>(p, split, s) : launch_bn<128, false>(p, split, s);
+    default: return cudaErrorInvalidValue;
+  }
+}
+
+}  // namespace nshb

@@ -420,6 +420,33 @@ struct Fp4Params {
   Fp4Item item[kMaxFp4];
 };
 
+// Products of 4-bit matrices (fp4_gemm.cu): D = P Q^T over tiles of P's rows (the accumulator's
+// lanes) x Q's rows (its columns).
+constexpr int kMaxFp4Prob = 48;
+constexpr int kFp4DTrans = 1;    // D element (p, q) goes to d[q * ld + p] (P is the caller's B), else d[p * ld + q]
+constexpr int kFp4DF32 = 2;      // D is fp32 (else bf16)
+constexpr int kFp4Sym = 4;       // P = Q: tiles on and below the diagonal, each also stored mirrored
+constexpr int kFp4DVec = 8;      // D's rows may be accessed 16 bytes at a time
+struct Fp4Prob {
+  CUtensorMap pc, qc;            // codes: rows x bytes, 128-byte swizzled boxes of 128 bytes (256 columns)
+  CUtensorMap ps, qs;            // scales: row tiles x column tiles x 512 bytes
+  const float *pg, *qg;          // NSHB_NVFP4: the matrices' scales, or NULL
+  void *d;
+  int64_t ld;
+  int32_t np, nq;                // extent of D that is stored
+  int32_t kt;                    // 256-column steps
+  int32_t qtiles;                // tiles along Q
+  int32_t tile_begin, flags;
+};
+struct Fp4GemmParams {
+  uint32_t *status;
+  long long wait_limit;
+  int32_t nprob, total_tiles;
+  int32_t clear_status;          // 1: the call owns the status word and the kernel's first CTA zeroes it
+  int32_t pad_;
+  Fp4Prob prob[kMaxFp4Prob];
+};
+
 // Launchers (defined in the .cu files); each returns cudaGetLastError().
 cudaError_t launch_momentum(const MomentumParams &p, cudaStream_t s);
 cudaError_t launch_norm_finalize(const NormFinParams &p, int nseg_total, cudaStream_t s);
@@ -452,6 +479,11 @@ cudaError_t launch_tens_finalize(const TensFinParams &p, cudaStream_t s);
 cudaError_t launch_tens_scale(const TensParams &p, cudaStream_t s);
 cudaError_t launch_fp4_quantize(const Fp4Params &p, bool transpose, cudaStream_t s);
 cudaError_t launch_fp4_dequantize(const Fp4Params &p, cudaStream_t s);
+// bn: Q rows of a tile (16, 32, 64, 128 or 256; below 128 only with one tile along Q); split: CTAs of a
+// cluster that share a tile's columns (1, 2, 4 or 8).
+cudaError_t launch_fp4_gemm(const Fp4GemmParams &p, int bn, int split, bool nv, cudaStream_t s);
+// Tensor maps of a 4-bit matrix for the products: `rows` rows a box, `srows` row tiles of scales a box.
+cudaError_t encode_fp4_maps(CUtensorMap *codes, CUtensorMap *scales, const nshb_fp4 &q, int rows, int srows);
 
 constexpr size_t kMaxParamBytes = 32764;   // kernel parameter limit (CUDA 12.1+, sm_70+)
 static_assert(sizeof(MomentumParams) <= kMaxParamBytes, "MomentumParams");
@@ -467,6 +499,7 @@ static_assert(sizeof(CholParams) <= kMaxParamBytes, "CholParams");
 static_assert(sizeof(NwParams) <= kMaxParamBytes, "NwParams");
 static_assert(sizeof(SplitParams) <= kMaxParamBytes, "SplitParams");
 static_assert(sizeof(Fp4Params) <= kMaxParamBytes, "Fp4Params");
+static_assert(sizeof(Fp4GemmParams) <= kMaxParamBytes, "Fp4GemmParams");
 static_assert(sizeof(TensParams) <= kMaxParamBytes, "TensParams");
 static_assert(sizeof(TensFinParams) <= kMaxParamBytes, "TensFinParams");
 static_assert(sizeof(DiagParams) <= kMaxParamBytes, "DiagParams");

@@ -165,3 +165,20 @@ def test_bad_quantize_arguments():
     assert quantize(x, q) == dequantize(q, x) == nshb.NSHB_ERR_DTYPE
     with pytest.raises(ValueError, match="1 4-bit matrices for 2"):
         nshb.fp4_quantize(fake((4, 5), (4, 5)), q)
+
+
+def matmul(a, b, d, ws=WS, ws_bytes=1 << 20, n=None):
+    return nshb.lib().nshb_fp4_matmul(a, b, d, d._n if n is None else n, ws, ws_bytes, None)
+
+
+def test_bad_products():
+    a, b, d = fake4((4, 70)), fake4((6, 70)), fake((4, 6))
+    assert matmul(a, b, fake((6, 4))) == matmul(a, None, d) == matmul(a, fake4((6, 69)), d) == nshb.NSHB_ERR_SHAPE
+    assert matmul(a, fake4((6, 70), fmt=nshb.NSHB_MXFP4), d) == nshb.NSHB_ERR_DTYPE
+    assert matmul(a, b, d, ws=None) == matmul(None, b, d) == matmul(a, b, None, n=1) == nshb.NSHB_ERR_NULL
+    assert matmul(a, b, d, ws_bytes=128) == matmul(a, b, d, ws=WS + 16) == nshb.NSHB_ERR_WORKSPACE
+    assert matmul(a, b, d, n=-1) == nshb.NSHB_ERR_SHAPE
+    b[0].codes = None
+    assert matmul(a, b, d) == nshb.NSHB_ERR_NULL
+    with pytest.raises(ValueError, match="operands"):
+        nshb.fp4_matmul(a, fake4((6, 70), (6, 70)), d, (WS, 1 << 20))
