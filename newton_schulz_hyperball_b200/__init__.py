@@ -344,29 +344,32 @@ def _device_of(handle):
     return getattr(handle, "_device", None)
 
 
-class _On:
-    """Runs a call with the tensors' device current and, unless one is given, its current stream."""
-    __slots__ = ("dev", "stream", "guard")
+def _current_stream(index: int) -> int:
+    """The handle of a device's current stream (torch.cuda.current_stream builds an object around it,
+    3 us of a call whose kernel may take as long)."""
+    import torch
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    return raw(index) if raw is not None else torch.cuda.current_stream(index).cuda_stream
 
-    def __init__(self, handle, stream, *others):
-        self.dev = _device_of(handle)
-        for what, t in others:
-            d = t.device if hasattr(t, "device") else _device_of(t)
-            if d is not None and self.dev is not None and d != self.dev:
-                raise ValueError(f"{what} is on {d}, the tensors on {self.dev}")
-        self.stream = stream
 
-    def __enter__(self):
-        import torch
-        self.guard = None
-        if self.dev is not None and self.dev.index != torch.cuda.current_device():
-            self.guard = torch.cuda.device(self.dev)
-            self.guard.__enter__()
-        return _stream(self.stream)
-
-    def __exit__(self, *a):
-        if self.guard is not None:
-            self.guard.__exit__(*a)
+def _on(name, handle, others, stream, *args):
+    """Calls the library's `name` with the device of `handle` (a tensors or fp4_matrices array) current, on
+    `stream` or that device's current stream; `others` (name, tensor or array) have to be on it."""
+    import torch
+    dev = _device_of(handle)
+    if dev is None:
+        _check(getattr(lib(), name)(*args, _stream(stream)), name)
+        return
+    for what, t in others:
+        d = getattr(t, "device", None) or _device_of(t)
+        if d is not None and d != dev:
+            raise ValueError(f"{what} is on {d}, the tensors on {dev}")
+    st = _current_stream(dev.index) if stream is None else _stream(stream)
+    if dev.index == torch.cuda.current_device():
+        _check(getattr(lib(), name)(*args, st), name)
+        return
+    with torch.cuda.device(dev):
+        _check(getattr(lib(), name)(*args, st), name)
 
 
 def grad_norm(g, total, ws, max_norm: float = float("inf"), each=None, kind: int = NSHB_NORM_L2, stream=None):
@@ -376,9 +379,8 @@ def grad_norm(g, total, ws, max_norm: float = float("inf"), each=None, kind: int
     _device_arg(total, "total", torch.float32, 2)
     _device_arg(each, "each", torch.float32, _n(g))
     ptr, nbytes = _ws(ws)
-    with _On(g, stream, ("total", total), ("each", each), ("workspace", ws)) as st:
-        _check(lib().nshb_grad_norm(g, _n(g), kind, max_norm, _ptr(total), _ptr(each), ptr, nbytes, st),
-               "nshb_grad_norm")
+    _on("nshb_grad_norm", g, (("total", total), ("each", each), ("workspace", ws)), stream,
+        g, _n(g), kind, max_norm, _ptr(total), _ptr(each), ptr, nbytes)
 
 
 def clip_grads(g, max_norm: float, total, ws, dst=None, kind: int = NSHB_NORM_L2, stream=None):
@@ -388,8 +390,8 @@ def clip_grads(g, max_norm: float, total, ws, dst=None, kind: int = NSHB_NORM_L2
     _device_arg(total, "total", torch.float32, 2)
     _same_count(g, dst)
     ptr, nbytes = _ws(ws)
-    with _On(g, stream, ("total", total), ("dst", dst), ("workspace", ws)) as st:
-        _check(lib().nshb_clip_grads(g, dst, _n(g), kind, max_norm, _ptr(total), ptr, nbytes, st), "nshb_clip_grads")
+    _on("nshb_clip_grads", g, (("total", total), ("dst", dst), ("workspace", ws)), stream,
+        g, dst, _n(g), kind, max_norm, _ptr(total), ptr, nbytes)
 
 
 def scale_grads(g, factor, dst=None, stream=None):
@@ -397,8 +399,7 @@ def scale_grads(g, factor, dst=None, stream=None):
     import torch
     _device_arg(factor, "factor", torch.float32, 1)
     _same_count(g, dst)
-    with _On(g, stream, ("factor", factor), ("dst", dst)) as st:
-        _check(lib().nshb_scale_grads(g, dst, _n(g), _ptr(factor), st), "nshb_scale_grads")
+    _on("nshb_scale_grads", g, (("factor", factor), ("dst", dst)), stream, g, dst, _n(g), _ptr(factor))
 
 
 def _same_count(a, b) -> None:
@@ -465,16 +466,15 @@ def fp4_quantize(x, q, ws=None, transpose: bool = False, stream=None):
     if _n(x) != _n(q):
         raise ValueError(f"{_n(q)} 4-bit matrices for {_n(x)} tensors")
     ptr, nbytes = (None, 0) if ws is None else _ws(ws)
-    with _On(x, stream, ("q", q), ("workspace", ws)) as st:
-        _check(lib().nshb_fp4_quantize(x, q, _n(x), 1 if transpose else 0, ptr, nbytes, st), "nshb_fp4_quantize")
+    _on("nshb_fp4_quantize", x, (("q", q), ("workspace", ws)), stream,
+        x, q, _n(x), 1 if transpose else 0, ptr, nbytes)
 
 
 def fp4_dequantize(q, x, stream=None):
     """The values of the 4-bit matrices `q` into the tensors `x`."""
     if _n(x) != _n(q):
         raise ValueError(f"{_n(x)} tensors for {_n(q)} 4-bit matrices")
-    with _On(q, stream, ("x", x)) as st:
-        _check(lib().nshb_fp4_dequantize(q, x, _n(q), st), "nshb_fp4_dequantize")
+    _on("nshb_fp4_dequantize", q, (("x", x),), stream, q, x, _n(q))
 
 
 def fp4_matmul(a, b, d, ws, stream=None):
@@ -483,8 +483,7 @@ def fp4_matmul(a, b, d, ws, stream=None):
     if _n(a) != _n(d) or (b is not None and _n(b) != _n(d)):
         raise ValueError(f"{_n(a)} and {_n(b) if b is not None else _n(a)} operands for {_n(d)} results")
     ptr, nbytes = _ws(ws)
-    with _On(d, stream, ("a", a), ("b", b), ("workspace", ws)) as st:
-        _check(lib().nshb_fp4_matmul(a, b, d, _n(d), ptr, nbytes, st), "nshb_fp4_matmul")
+    _on("nshb_fp4_matmul", d, (("a", a), ("b", b), ("workspace", ws)), stream, a, b, d, _n(d), ptr, nbytes)
 
 
 def device_status(ws, stream=None) -> int:

@@ -165,7 +165,8 @@ __device__ __forceinline__ uint32_t quantize32(const Cols32<F32> &v, int eg, uin
   return scales;
 }
 
-__device__ __forceinline__ int find_item(const Fp4Params &p, int tile) {
+template <class P>
+__device__ __forceinline__ int find_item(const P &p, int tile) {
   int lo = 0, hi = p.n - 1;
   while (lo < hi) {
     const int mid = (lo + hi + 1) >> 1;
@@ -277,8 +278,8 @@ __device__ __forceinline__ void quantize_tile_t(const Fp4Item &q, int tr, int tk
   }
 }
 
-template <bool TRANS>
-__global__ void __launch_bounds__(kThreads) fp4_quantize_kernel(const __grid_constant__ Fp4Params p) {
+template <bool TRANS, int N>
+__global__ void __launch_bounds__(kThreads) fp4_quantize_kernel(const __grid_constant__ Fp4Block<N> p) {
   extern __shared__ uint32_t tile[];
   __shared__ __align__(16) uint8_t stage[1024];
   __shared__ uint32_t tops[kThreads / 32];
@@ -314,7 +315,8 @@ __global__ void __launch_bounds__(kThreads) fp4_quantize_kernel(const __grid_con
 }
 
 // Values of 32 columns, two rows a thread.
-__global__ void __launch_bounds__(kThreads) fp4_dequantize_kernel(const __grid_constant__ Fp4Params p) {
+template <int N>
+__global__ void __launch_bounds__(kThreads) fp4_dequantize_kernel(const __grid_constant__ Fp4Block<N> p) {
   pdl_trigger();
   pdl_wait();
   const Fp4Item &q = p.item[find_item(p, blockIdx.x)];
@@ -375,11 +377,10 @@ __global__ void __launch_bounds__(kThreads) fp4_dequantize_kernel(const __grid_c
 
 constexpr int kTileBytesT = kT * 128 * 4;   // an fp32 tile of the transposing kernel
 
-}  // namespace
-
-cudaError_t launch_fp4_quantize(const Fp4Params &p, bool transpose, cudaStream_t s) {
-  if (p.total_tiles <= 0) return cudaSuccess;
-  if (!transpose) return launch_pdl(fp4_quantize_kernel<false>, dim3(p.total_tiles), dim3(kThreads), 0, s, p);
+template <int N>
+cudaError_t launch_quantize(const Fp4Params &p, bool transpose, cudaStream_t s) {
+  const Fp4Block<N> &b = prefix<Fp4Block<N>>(p);
+  if (!transpose) return launch_pdl(fp4_quantize_kernel<false, N>, dim3(p.total_tiles), dim3(kThreads), 0, s, b);
   bool f32 = false;
   for (int i = 0; i < p.n; ++i) f32 = f32 || (p.item[i].flags & kFp4F32);
   static PerDevice attr_set;
@@ -387,16 +388,25 @@ cudaError_t launch_fp4_quantize(const Fp4Params &p, bool transpose, cudaStream_t
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (f32 && !attr_set.get(dev)) {
-    e = cudaFuncSetAttribute(fp4_quantize_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, kTileBytesT);
+    e = cudaFuncSetAttribute(fp4_quantize_kernel<true, N>, cudaFuncAttributeMaxDynamicSharedMemorySize, kTileBytesT);
     if (e != cudaSuccess) return e;
     attr_set.set(dev, 1);
   }
-  return launch_pdl(fp4_quantize_kernel<true>, dim3(p.total_tiles), dim3(kThreads), f32 ? kTileBytesT : kTileBytesT / 2, s, p);
+  return launch_pdl(fp4_quantize_kernel<true, N>, dim3(p.total_tiles), dim3(kThreads), f32 ? kTileBytesT : kTileBytesT / 2, s, b);
+}
+
+}  // namespace
+
+cudaError_t launch_fp4_quantize(const Fp4Params &p, bool transpose, cudaStream_t s) {
+  if (p.total_tiles <= 0) return cudaSuccess;
+  return p.n <= kFewFp4 ? launch_quantize<kFewFp4>(p, transpose, s) : launch_quantize<kMaxFp4>(p, transpose, s);
 }
 
 cudaError_t launch_fp4_dequantize(const Fp4Params &p, cudaStream_t s) {
   if (p.total_tiles <= 0) return cudaSuccess;
-  return launch_pdl(fp4_dequantize_kernel, dim3(p.total_tiles), dim3(kThreads), 0, s, p);
+  if (p.n <= kFewFp4)
+    return launch_pdl(fp4_dequantize_kernel<kFewFp4>, dim3(p.total_tiles), dim3(kThreads), 0, s, prefix<Fp4Block<kFewFp4>>(p));
+  return launch_pdl(fp4_dequantize_kernel<kMaxFp4>, dim3(p.total_tiles), dim3(kThreads), 0, s, p);
 }
 
 }  // namespace nshb

@@ -101,7 +101,7 @@ nshb_status run_fp4_products(const nshb_fp4 *A, const nshb_fp4 *B, const nshb_te
   int32_t i = 0;
   while (i < n) {
     Fp4GemmParams p;
-    std::memset(&p, 0, offsetof(Fp4GemmParams, prob));
+    std::memset(static_cast<Fp4GemmHead *>(&p), 0, sizeof(Fp4GemmHead));
     p.status = status;
     p.wait_limit = limit;
     p.clear_status = clear;
@@ -185,7 +185,7 @@ nshb_status nshb_fp4_quantize(const nshb_tensor *X, const nshb_fp4 *Q, int32_t n
   cudaStream_t st = (cudaStream_t)stream;
   for (int32_t i = 0; i < n;) {
     Fp4Params p;
-    std::memset(&p, 0, offsetof(Fp4Params, item));
+    std::memset(static_cast<Fp4Head *>(&p), 0, sizeof(Fp4Head));
     nshb_tensor src[kMaxFp4];     // the NVFP4 items' sources, whose largest magnitudes come first
     int32_t of[kMaxFp4], n_src = 0;
     int64_t tiles = 0;
@@ -223,7 +223,7 @@ nshb_status nshb_fp4_dequantize(const nshb_fp4 *Q, const nshb_tensor *X, int32_t
   cudaStream_t st = (cudaStream_t)stream;
   for (int32_t i = 0; i < n;) {
     Fp4Params p;
-    std::memset(&p, 0, offsetof(Fp4Params, item));
+    std::memset(static_cast<Fp4Head *>(&p), 0, sizeof(Fp4Head));
     int64_t tiles = 0;
     for (; i < n && p.n < kMaxFp4; ++i) {
       if (Q[i].rows == 0 || Q[i].cols == 0) continue;

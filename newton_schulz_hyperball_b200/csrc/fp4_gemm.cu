@@ -47,7 +47,8 @@ struct Cfg {
   static_assert(128 * BN * 4 <= kStages * kStage, "the partial sums fit the ring");
 };
 
-__device__ __forceinline__ int find_prob(const Fp4GemmParams &p, int tile) {
+template <class P>
+__device__ __forceinline__ int find_prob(const P &p, int tile) {
   int lo = 0, hi = p.nprob - 1;
   while (lo < hi) {
     const int mid = (lo + hi + 1) >> 1;
@@ -107,8 +108,8 @@ __device__ __forceinline__ void store_row(const Fp4Prob &q, int64_t p, int64_t q
   }
 }
 
-template <int BN, bool NV, bool SPLIT>
-__global__ void __launch_bounds__(kThreads, BN > 128 ? 1 : 2) fp4_gemm_kernel(const __grid_constant__ Fp4GemmParams p) {
+template <int BN, bool NV, bool SPLIT, int NP>
+__global__ void __launch_bounds__(kThreads, BN > 128 ? 1 : 2) fp4_gemm_kernel(const __grid_constant__ Fp4GemmBlock<NP> p) {
   using C = Cfg<BN, NV>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -315,7 +316,7 @@ __global__ void __launch_bounds__(kThreads, BN > 128 ? 1 : 2) fp4_gemm_kernel(co
   }
 }
 
-template <int BN, bool NV, bool SPLIT>
+template <int BN, bool NV, bool SPLIT, int NP>
 cudaError_t launch(const Fp4GemmParams &p, int split, cudaStream_t s) {
   using C = Cfg<BN, NV>;
   static PerDevice attr_set;
@@ -323,7 +324,7 @@ cudaError_t launch(const Fp4GemmParams &p, int split, cudaStream_t s) {
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (!attr_set.get(dev)) {
-    e = cudaFuncSetAttribute(fp4_gemm_kernel<BN, NV, SPLIT>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+    e = cudaFuncSetAttribute(fp4_gemm_kernel<BN, NV, SPLIT, NP>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
     if (e != cudaSuccess) return e;
     attr_set.set(dev, 1);
   }
@@ -341,13 +342,15 @@ cudaError_t launch(const Fp4GemmParams &p, int split, cudaStream_t s) {
   attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = SPLIT ? 2 : 1;
-  e = cudaLaunchKernelEx(&cfg, fp4_gemm_kernel<BN, NV, SPLIT>, p);
+  e = cudaLaunchKernelEx(&cfg, fp4_gemm_kernel<BN, NV, SPLIT, NP>, prefix<Fp4GemmBlock<NP>>(p));
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 
 template <int BN, bool NV>
 cudaError_t launch_bn(const Fp4GemmParams &p, int split, cudaStream_t s) {
-  return split > 1 ? launch<BN, NV, true>(p, split, s) : launch<BN, NV, false>(p, 1, s);
+  if (p.nprob <= kFewFp4Prob)
+    return split > 1 ? launch<BN, NV, true, kFewFp4Prob>(p, split, s) : launch<BN, NV, false, kFewFp4Prob>(p, 1, s);
+  return split > 1 ? launch<BN, NV, true, kMaxFp4Prob>(p, split, s) : launch<BN, NV, false, kMaxFp4Prob>(p, 1, s);
 }
 
 }  // namespace

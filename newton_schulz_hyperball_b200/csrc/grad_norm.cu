@@ -9,6 +9,8 @@
 // keeps its sum in registers and reduces it only where its share of a tensor ends.
 #include <cuda_runtime.h>
 
+#include <type_traits>
+
 #include "nshb_device.cuh"
 #include "nshb_internal.h"
 
@@ -201,7 +203,8 @@ __device__ __forceinline__ double norm_windows(const TensRec &q, int w, int wend
   return v.value();
 }
 
-__device__ __forceinline__ int find_tensor(const TensParams &p, int win) {
+template <class P>
+__device__ __forceinline__ int find_tensor(const P &p, int win) {
   int lo = 0, hi = p.ntens - 1;
   while (lo < hi) {
     const int mid = (lo + hi + 1) >> 1;
@@ -215,8 +218,8 @@ __device__ __forceinline__ int find_tensor(const TensParams &p, int win) {
 // tensor; where both borders meet it grows by two, and the record between is set to zero.  So the
 // records are a list without gaps in a fixed order, tensor t's are consecutive, and their number does
 // not depend on the sizes.
-template <class V>
-__device__ __forceinline__ void norm_line(const TensParams &p) {
+template <class V, class P>
+__device__ __forceinline__ void norm_line(const P &p) {
   __shared__ double scratch[kThreads / 32];
   const int c = blockIdx.x;
   const int w0 = (int)((int64_t)c * p.nwin / p.nctas), w1 = (int)((int64_t)(c + 1) * p.nwin / p.nctas);
@@ -236,7 +239,8 @@ __device__ __forceinline__ void norm_line(const TensParams &p) {
   }
 }
 
-__global__ void __launch_bounds__(kThreads, kNormCtasPerSm) tens_norm_kernel(const __grid_constant__ TensParams p) {
+template <int N>
+__global__ void __launch_bounds__(kThreads, kNormCtasPerSm) tens_norm_kernel(const __grid_constant__ TensBlock<N> p) {
   pdl_trigger();
   pdl_wait();
   if (p.kind == kNormL2) norm_line<SumSquares>(p);
@@ -244,21 +248,37 @@ __global__ void __launch_bounds__(kThreads, kNormCtasPerSm) tens_norm_kernel(con
   else norm_line<LargestBits<true>>(p);
 }
 
-// One CTA: the norms of the tensors (where asked for) and of the whole.
-__global__ void __launch_bounds__(kThreads) tens_finalize_kernel(const __grid_constant__ TensFinParams p) {
+// One CTA: the norms of the tensors (where asked for) and of the whole.  A tensor's records are
+// summed by a thread where they are few, by a warp otherwise.
+template <int N>
+__global__ void __launch_bounds__(kThreads) tens_finalize_kernel(const __grid_constant__ TensFinBlock<N> p) {
   __shared__ double scratch[kThreads / 32];
   pdl_trigger();
   pdl_wait();
   if (p.each) {
     const int lane = threadIdx.x & 31;
-    for (int k = threadIdx.x >> 5; k < p.ntens; k += kThreads / 32) {
-      const int c0 = win_cta(p.win_begin[k], p.nwin, p.nctas), c1 = win_cta(p.win_begin[k + 1] - 1, p.nwin, p.nctas);
+    for (int k0 = (int)(threadIdx.x & ~31u); k0 < p.ntens; k0 += kThreads) {
+      const int k = k0 + lane;
+      int c0 = 0, n = 0;
+      if (k < p.ntens) {
+        const int end = k + 1 < p.ntens ? p.at[k + 1].win_begin : p.nwin;
+        c0 = win_cta(p.at[k].win_begin, p.nwin, p.nctas);
+        n = win_cta(end - 1, p.nwin, p.nctas) - c0 + 1;
+      }
       double v = 0.0;
-      for (int c = c0 + lane; c <= c1; c += 32) v = join(p.kind, v, p.rec[c + k]);
-      v = warp_join(p.kind, v);
-      if (lane == 0) p.each[p.index[k]] = norm_of(p.kind, v);
+      if (n <= 8)
+        for (int i = 0; i < n; ++i) v = join(p.kind, v, p.rec[c0 + k + i]);
+      for (unsigned many = __ballot_sync(0xffffffffu, n > 8); many; many &= many - 1) {
+        const int src = __ffs(many) - 1;
+        const int first = __shfl_sync(0xffffffffu, c0 + k, src), count = __shfl_sync(0xffffffffu, n, src);
+        double s = 0.0;
+        for (int i = lane; i < count; i += 32) s = join(p.kind, s, p.rec[first + i]);
+        s = warp_join(p.kind, s);
+        if (lane == src) v = s;
+      }
+      if (k < p.ntens) p.each[p.at[k].index] = norm_of(p.kind, v);
     }
-    for (int k = p.ntens + threadIdx.x; k < p.ntens + p.n_empty; k += kThreads) p.each[p.index[k]] = 0.f;
+    for (int k = p.ntens + threadIdx.x; k < p.ntens + p.n_empty; k += kThreads) p.each[p.at[k].index] = 0.f;
   }
   double v = join_records(p.kind, p.rec, p.ntens ? p.nctas + p.ntens - 1 : 0, scratch);
   if (threadIdx.x == 0) {
@@ -338,7 +358,8 @@ __device__ __forceinline__ void scale_windows(const TensRec &q, int w, int wend,
 
 // The factor is read, or formed from the norm's records by every CTA for itself (a few KB from L2,
 // no launch between the norm and the scaling).
-__global__ void __launch_bounds__(kThreads, kScaleCtasPerSm) tens_scale_kernel(const __grid_constant__ TensParams p) {
+template <int N>
+__global__ void __launch_bounds__(kThreads, kScaleCtasPerSm) tens_scale_kernel(const __grid_constant__ TensBlock<N> p) {
   __shared__ double scratch[kThreads / 32];
   pdl_trigger();
   pdl_wait();
@@ -375,18 +396,35 @@ __global__ void __launch_bounds__(kThreads, kScaleCtasPerSm) tens_scale_kernel(c
 
 }  // namespace
 
+// Calls launch(capacity) with the smallest instance that holds `n` records.
+template <class F>
+static cudaError_t with_capacity(int n, F &&launch) {
+  if (n <= kFewTens) return launch(std::integral_constant<int, kFewTens>());
+  if (n <= kSomeTens) return launch(std::integral_constant<int, kSomeTens>());
+  return launch(std::integral_constant<int, kMaxTens>());
+}
+
 cudaError_t launch_tens_norm(const TensParams &p, cudaStream_t s) {
   if (p.nwin <= 0) return cudaSuccess;
-  return launch_pdl(tens_norm_kernel, dim3(p.nctas), dim3(kThreads), 0, s, p);
+  return with_capacity(p.ntens, [&](auto n) {
+    constexpr int N = decltype(n)::value;
+    return launch_pdl(tens_norm_kernel<N>, dim3(p.nctas), dim3(kThreads), 0, s, prefix<TensBlock<N>>(p));
+  });
 }
 
 cudaError_t launch_tens_finalize(const TensFinParams &p, cudaStream_t s) {
-  return launch_pdl(tens_finalize_kernel, dim3(1), dim3(kThreads), 0, s, p);
+  return with_capacity(p.ntens + p.n_empty, [&](auto n) {
+    constexpr int N = decltype(n)::value;
+    return launch_pdl(tens_finalize_kernel<N>, dim3(1), dim3(kThreads), 0, s, prefix<TensFinBlock<N>>(p));
+  });
 }
 
 cudaError_t launch_tens_scale(const TensParams &p, cudaStream_t s) {
   if (p.nwin <= 0) return cudaSuccess;
-  return launch_pdl(tens_scale_kernel, dim3(p.nctas), dim3(kThreads), 0, s, p);
+  return with_capacity(p.ntens, [&](auto n) {
+    constexpr int N = decltype(n)::value;
+    return launch_pdl(tens_scale_kernel<N>, dim3(p.nctas), dim3(kThreads), 0, s, prefix<TensBlock<N>>(p));
+  });
 }
 
 }  // namespace nshb

@@ -92,6 +92,13 @@ inline cudaError_t launch_pdl(void (*kernel)(KArgs...), dim3 grid, dim3 block, s
   return cudaLaunchKernelEx(&cfg, kernel, static_cast<Args &&>(args)...);
 }
 
+// The beginning of a parameter block as the smaller block that an instance takes.
+template <class S, class L>
+inline const S &prefix(const L &large) {
+  static_assert(sizeof(S) <= sizeof(L), "a prefix");
+  return reinterpret_cast<const S &>(large);
+}
+
 // ------------------------------------------------------------ shared-memory addresses
 __device__ __forceinline__ uint32_t smem_u32(const void *p) {
   return static_cast<uint32_t>(__cvta_generic_to_shared(p));

@@ -369,7 +369,7 @@ struct TensRec {
   int32_t per_row;         // kTensRun: windows a run; else rows a window
   int32_t flags;
 };
-struct TensParams {
+struct TensHead {
   double *rec;             // norm: one record per (CTA, tensor) step of the line, see tens_norm_kernel
   const double *coef_rec;  // scale: the records of the whole set (factor formed from them), or NULL
   const float *factor;     // scale: the factor, where coef_rec is NULL
@@ -379,10 +379,18 @@ struct TensParams {
   int32_t kind;            // kNormL2 ...
   int32_t n_rec;           // records behind coef_rec
   int32_t ntens, nwin, nctas;
-  TensRec t[kMaxTens];
 };
+// A launch's parameter block: the head and as many records as the kernel's instance holds.  The host fills
+// the largest; a small list launches an instance that takes the beginning of it, since the bytes of
+// the parameter block are time on the host and on the GPU (28 KB against 2 KB: about 2 us a launch).
+template <int N>
+struct TensBlock : TensHead {
+  TensRec t[N];
+};
+constexpr int kFewTens = 32, kSomeTens = 160;
+using TensParams = TensBlock<kMaxTens>;
 enum NormKind { kNormL2 = 0, kNormInf = 1, kNormFinite = 2 };   // kNormFinite: largest finite magnitude
-struct TensFinParams {
+struct TensFinHead {
   const double *rec;       // records of this launch's tensors
   double *acc;             // the running value over the launches of one call
   float *total, *each;
@@ -390,9 +398,16 @@ struct TensFinParams {
   float max_norm;
   int32_t kind, first, last;
   int32_t ntens, n_empty, nwin, nctas;
-  int32_t win_begin[kMaxTens + 1];
-  int32_t index[kMaxTens]; // where tensor k's norm goes in `each`; the last n_empty have no elements
 };
+struct TensPlace {
+  int32_t win_begin;       // first window of tensor k (nwin for those without elements)
+  int32_t index;           // where its norm goes in `each`
+};
+template <int N>
+struct TensFinBlock : TensFinHead {
+  TensPlace at[N];         // the ntens with elements, then the n_empty without
+};
+using TensFinParams = TensFinBlock<kMaxTens>;
 // The CTA of `nctas` that takes window w of a line of nwin: CTA c takes [c nwin / nctas, (c + 1) nwin / nctas).
 __host__ __device__ inline int win_cta(int w, int nwin, int nctas) {
   return (int)((((int64_t)w + 1) * nctas - 1) / nwin);
@@ -414,11 +429,16 @@ struct Fp4Item {
   int32_t flags;
   int32_t rec_begin, n_rec;   // kFp4Nv: records of the source's largest magnitude
 };
-struct Fp4Params {
+struct Fp4Head {
   const double *rec;
   int32_t n, total_tiles;
-  Fp4Item item[kMaxFp4];
 };
+template <int N>
+struct Fp4Block : Fp4Head {
+  Fp4Item item[N];         // see TensBlock
+};
+constexpr int kFewFp4 = 16;
+using Fp4Params = Fp4Block<kMaxFp4>;
 
 // Products of 4-bit matrices (fp4_gemm.cu): D = P Q^T over tiles of P's rows (the accumulator's
 // lanes) x Q's rows (its columns).
@@ -438,14 +458,19 @@ struct Fp4Prob {
   int32_t qtiles;                // tiles along Q
   int32_t tile_begin, flags;
 };
-struct Fp4GemmParams {
+struct Fp4GemmHead {
   uint32_t *status;
   long long wait_limit;
   int32_t nprob, total_tiles;
   int32_t clear_status;          // 1: the call owns the status word and the kernel's first CTA zeroes it
   int32_t pad_;
-  Fp4Prob prob[kMaxFp4Prob];
 };
+template <int N>
+struct Fp4GemmBlock : Fp4GemmHead {
+  Fp4Prob prob[N];         // see TensBlock
+};
+constexpr int kFewFp4Prob = 4;
+using Fp4GemmParams = Fp4GemmBlock<kMaxFp4Prob>;
 
 // Launchers (defined in the .cu files); each returns cudaGetLastError().
 cudaError_t launch_momentum(const MomentumParams &p, cudaStream_t s);

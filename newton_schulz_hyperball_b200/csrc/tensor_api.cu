@@ -110,16 +110,15 @@ nshb_status fill_launch(const nshb_tensor *src, const nshb_tensor *dst, int32_t 
       break;
     }
     if (fin) {
-      fin->index[p.ntens] = i;
-      fin->win_begin[p.ntens] = p.t[p.ntens].win_begin;
+      fin->at[p.ntens].index = i;
+      fin->at[p.ntens].win_begin = p.t[p.ntens].win_begin;
     }
     ++p.ntens;
   }
   p.nwin = (int32_t)win;
   p.nctas = tens_ctas(p.nwin, dst ? kScaleCtasPerSm : kNormCtasPerSm);
   if (fin) {
-    for (int32_t k = 0; k < n_empty; ++k) fin->index[p.ntens + k] = empty[k];
-    fin->win_begin[p.ntens] = p.nwin;
+    for (int32_t k = 0; k < n_empty; ++k) fin->at[p.ntens + k] = {p.nwin, empty[k]};
     fin->ntens = p.ntens;
     fin->n_empty = n_empty;
     fin->nwin = p.nwin;
@@ -136,9 +135,9 @@ nshb_status run_norm(const nshb_tensor *g, int32_t n, int32_t kind, float max_no
   bool first = true;
   do {
     TensParams p;
-    std::memset(&p, 0, offsetof(TensParams, t));
+    std::memset(static_cast<TensHead *>(&p), 0, sizeof(TensHead));
     TensFinParams f;
-    std::memset(&f, 0, offsetof(TensFinParams, win_begin));
+    std::memset(static_cast<TensFinHead *>(&f), 0, sizeof(TensFinHead));
     const nshb_status e = fill_launch(g, nullptr, n, i, p, &f);
     if (e != NSHB_OK) return e;
     p.rec = w.rec;
@@ -168,7 +167,7 @@ nshb_status run_scale(const nshb_tensor *src, const nshb_tensor *dst, int32_t n,
                       float max_norm, float *total, const TensWorkspace *w, int32_t n_rec, cudaStream_t st) {
   for (int32_t i = 0; i < n;) {
     TensParams p;
-    std::memset(&p, 0, offsetof(TensParams, t));
+    std::memset(static_cast<TensHead *>(&p), 0, sizeof(TensHead));
     const nshb_status e = fill_launch(src, dst ? dst : src, n, i, p, nullptr);
     if (e != NSHB_OK) return e;
     p.factor = factor;
@@ -191,7 +190,7 @@ nshb_status run_largest(const nshb_tensor *t, int32_t n, const TensWorkspace &w,
                         int32_t *n_rec) {
   int32_t i = 0;
   TensParams p;
-  std::memset(&p, 0, offsetof(TensParams, t));
+  std::memset(static_cast<TensHead *>(&p), 0, sizeof(TensHead));
   const nshb_status e = fill_launch(t, nullptr, n, i, p, nullptr);
   if (e != NSHB_OK) return e;
   if (i != n) return NSHB_ERR_UNSUPPORTED;
