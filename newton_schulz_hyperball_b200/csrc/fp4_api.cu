@@ -64,8 +64,14 @@ struct Shape {
   int64_t tiles;
 };
 
-Shape shape_of(int64_t m, int64_t n, int64_t kt, bool sym) {
+Shape shape_of(int64_t m, int64_t n, int64_t kt, bool sym, bool pairs) {
   Shape s = {128, 1, false, 0};
+  if (pairs && kt > 0 && std::min(m, n) > 128) {
+    const int64_t pt = (m + 255) / 256, qt = (n + 255) / 256;
+    s.bn = 256;
+    s.tiles = sym ? pt * (pt + 1) / 2 : pt * qt;
+    return s;
+  }
   int64_t p = m, q = n;
   if (!sym && std::min(m, n) <= 64) {
     s.swap = m < n;
@@ -98,6 +104,13 @@ nshb_status check_products(const nshb_fp4 *A, const nshb_fp4 *B, const nshb_tens
 // Products of one launch; `d` as the caller stores it.  See launch_fp4_gemm for what the launches share.
 nshb_status run_fp4_products(const nshb_fp4 *A, const nshb_fp4 *B, const nshb_tensor *D, int32_t n, uint32_t *status,
                              bool clear, long long limit, cudaStream_t st) {
+  int64_t wide = 0;   // 256 x 256 tiles of the call
+  for (int32_t i = 0; i < n; ++i)
+    if (D[i].rows && D[i].cols) {
+      const Shape s = shape_of(D[i].rows, D[i].cols, (A[i].cols + 255) / 256, !B, true);
+      wide += s.bn == 256 ? s.tiles : 0;
+    }
+  const bool pairs = wide >= device_sms() / 2;
   int32_t i = 0;
   while (i < n) {
     Fp4GemmParams p;
@@ -113,7 +126,7 @@ nshb_status run_fp4_products(const nshb_fp4 *A, const nshb_fp4 *B, const nshb_te
       if (D[i].rows == 0 || D[i].cols == 0) continue;
       const int64_t kt = (a.cols + 255) / 256;
       const bool sym = !B;
-      const Shape s = shape_of(D[i].rows, D[i].cols, kt, sym);
+      const Shape s = shape_of(D[i].rows, D[i].cols, kt, sym, pairs);
       if (p.nprob && (s.bn != first.bn || s.split != first.split || a.format != format)) break;
       if ((tiles + s.tiles) * s.split > (1LL << 30)) {
         if (p.nprob) break;
@@ -126,7 +139,8 @@ nshb_status run_fp4_products(const nshb_fp4 *A, const nshb_fp4 *B, const nshb_te
       const nshb_fp4 &P = s.swap ? b : a, &Q = s.swap ? a : b;
       if (kt) {
         cudaError_t e = encode_fp4_maps(&q.pc, &q.ps, P, 128, 1);
-        if (e == cudaSuccess) e = encode_fp4_maps(&q.qc, &q.qs, Q, s.bn, 1);
+        if (e == cudaSuccess)
+          e = s.bn == 256 ? encode_fp4_maps(&q.qc, &q.qs, Q, 128, 2) : encode_fp4_maps(&q.qc, &q.qs, Q, s.bn, 1);
         if (e != cudaSuccess) {
           record_cuda_error(e);
           return NSHB_ERR_CUDA;

@@ -12,7 +12,10 @@
 // and a cluster of up to 8 CTAs shares the columns of one tile, each summing its part; the parts are joined
 // through distributed shared memory in a fixed order.
 //
-// Roles (192 threads): warp 0 issues the loads of the ring, warp 1 the copies and MMAs, warps
+// Enough 256 x 256 tiles to fill the GPU go to CTA pairs (fp4_pair_kernel): a pair reads 64 bytes of
+// codes per clock and SM for the work that single CTAs with 128 x 128 tiles need 128 for.
+//
+// Roles of the single CTA (192 threads): warp 0 issues the loads of the ring, warp 1 the copies and MMAs, warps
 // 2-5 drain the accumulator.  Every wait is bounded.
 #include <cuda.h>
 #include <cuda_runtime.h>
@@ -32,17 +35,16 @@ constexpr uint32_t kTimeoutBit = 0x4u;
 template <int BN, bool NV>
 struct Cfg {
   static constexpr int kSTiles = NV ? 4 : 2;                 // 512-byte scale tiles of a step and 128 rows
-  static constexpr int kQRowTiles = BN > 128 ? 2 : 1;
   static constexpr int kPBytes = 128 * 128, kQBytes = BN * 128;
-  static constexpr int kPs = kSTiles * 512, kQs = kSTiles * 512 * kQRowTiles;
+  static constexpr int kPs = kSTiles * 512, kQs = kSTiles * 512;
   static constexpr int kStage = kPBytes + kQBytes + kPs + kQs;   // a multiple of 1024
-  // two CTAs on an SM up to BN = 128
-  static constexpr int kStages = BN > 128 ? 4 : 110 * 1024 / kStage;
+  // two CTAs on an SM
+  static constexpr int kStages = 110 * 1024 / kStage;
   static constexpr int kSmem = kStages * kStage + 1024 + 256;
   static constexpr int kPsCol = BN < 32 ? 32 : BN;           // TMEM columns: accumulator, P's scales, Q's
   static constexpr int kQsCol = kPsCol + 4 * kSTiles;
-  static constexpr int kUsed = kQsCol + 4 * kSTiles * kQRowTiles;
-  static constexpr int kTmem = kUsed <= 64 ? 64 : kUsed <= 128 ? 128 : kUsed <= 256 ? 256 : 512;
+  static constexpr int kUsed = kQsCol + 4 * kSTiles;
+  static constexpr int kTmem = kUsed <= 64 ? 64 : kUsed <= 128 ? 128 : 256;
   static_assert(kStage % 1024 == 0, "every stage starts on a swizzle atom");
   static_assert(128 * BN * 4 <= kStages * kStage, "the partial sums fit the ring");
 };
@@ -109,7 +111,7 @@ __device__ __forceinline__ void store_row(const Fp4Prob &q, int64_t p, int64_t q
 }
 
 template <int BN, bool NV, bool SPLIT, int NP>
-__global__ void __launch_bounds__(kThreads, BN > 128 ? 1 : 2) fp4_gemm_kernel(const __grid_constant__ Fp4GemmBlock<NP> p) {
+__global__ void __launch_bounds__(kThreads, 2) fp4_gemm_kernel(const __grid_constant__ Fp4GemmBlock<NP> p) {
   using C = Cfg<BN, NV>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -178,7 +180,7 @@ __global__ void __launch_bounds__(kThreads, BN > 128 ? 1 : 2) fp4_gemm_kernel(co
         tma_load_2d(sp, &q.pc, kb * 128, pt * 128, full(stage));
         tma_load_2d(sq, &q.qc, kb * 128, qt * BN, full(stage));
         tma_load_3d(ss, &q.ps, 0, kb * C::kSTiles, pt, full(stage));
-        tma_load_3d(ss + C::kPs, &q.qs, 0, kb * C::kSTiles, qt * C::kQRowTiles, full(stage));
+        tma_load_3d(ss + C::kPs, &q.qs, 0, kb * C::kSTiles, qt, full(stage));
         if (++stage == C::kStages) {
           stage = 0;
           phase ^= 1u;
@@ -205,17 +207,14 @@ __global__ void __launch_bounds__(kThreads, BN > 128 ? 1 : 2) fp4_gemm_kernel(co
 #pragma unroll
         for (int j = 0; j < C::kSTiles; ++j) {
           tc_cp_scales(tmem + C::kPsCol + 4 * j, smem_desc_scales(ss + 512 * j));
-#pragma unroll
-          for (int i = 0; i < C::kQRowTiles; ++i)
-            tc_cp_scales(tmem + C::kQsCol + 4 * (C::kQRowTiles * j + i),
-                         smem_desc_scales(ss + C::kPs + 512 * (C::kSTiles * i + j)));
+          tc_cp_scales(tmem + C::kQsCol + 4 * j, smem_desc_scales(ss + C::kPs + 512 * j));
         }
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
           // 64 columns: 32 bytes inside the swizzled rows; MX: half of a scale word, NV: a whole one
           const int j = NV ? k : k >> 1, id = NV ? 0 : 2 * (k & 1);
           tc_mma_fp4<NV>(tmem, smem_desc_sw128(sp + 32 * k, 16, 1024), smem_desc_sw128(sq + 32 * k, 16, 1024),
-                         idesc_fp4(128, BN, NV, id), tmem + C::kPsCol + 4 * j, tmem + C::kQsCol + 4 * C::kQRowTiles * j,
+                         idesc_fp4(128, BN, NV, id), tmem + C::kPsCol + 4 * j, tmem + C::kQsCol + 4 * j,
                          kb != k0 || k != 0);
         }
         tc_commit(empty(stage));
@@ -316,6 +315,246 @@ __global__ void __launch_bounds__(kThreads, BN > 128 ? 1 : 2) fp4_gemm_kernel(co
   }
 }
 
+// 256 x 256 tiles on CTA pairs, persistent.  The accumulator of the next tile starts 192 columns after (or
+// before) that of this one: two of 256 columns and the scales do not fit the 512 of tensor memory.
+// So the epilogue drains the 64 shared columns first and hands them over at once; the next tile's MMAs run
+// beside the rest of it.
+template <bool NV>
+struct PairCfg {
+  static constexpr int kSTiles = NV ? 4 : 2;
+  static constexpr int kHalf = 128 * 128;                    // codes of 128 rows
+  static constexpr int kPs = kSTiles * 512, kQs = 2 * kPs;   // P's own rows, all of Q's
+  static constexpr int kStage = 2 * kHalf + kPs + kQs;       // of one CTA
+  static constexpr int kStages = NV ? 5 : 6;
+  static constexpr int kSmem = kStages * kStage + 1024 + 256;
+  static constexpr int kStep = 192;                          // between the two accumulators
+  static constexpr int kPsCol = 448, kQsCol = kPsCol + 4 * kSTiles;
+  static_assert(kStage % 1024 == 0 && kQsCol + 8 * kSTiles <= 512 && kSmem <= 232448, "fits");
+};
+constexpr int kPairEpiWarps = 8;
+constexpr int kPairThreads = 64 + 32 * kPairEpiWarps;
+constexpr uint32_t kPeerMask = 0xFEFFFFFFu;                  // clears the CTA-rank bit of a cluster address
+
+template <bool NV, int NP>
+__global__ void __launch_bounds__(kPairThreads, 1) fp4_pair_kernel(const __grid_constant__ Fp4GemmBlock<NP> p) {
+  using C = PairCfg<NV>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint64_t *bars = reinterpret_cast<uint64_t *>(smem + C::kStages * C::kStage);
+  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + 2 * C::kStages + 2);
+  const uint32_t base = smem_u32(smem), bar_base = smem_u32(bars);
+  auto full = [&](int s) { return bar_base + 8u * s; };
+  auto empty = [&](int s) { return bar_base + 8u * (C::kStages + s); };
+  const uint32_t tfull = bar_base + 8u * (2 * C::kStages), tfree = tfull + 8u;
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = cta_rank();
+  const bool leader = rank == 0;
+  const int cid = (int)cluster_id(), ncl = (int)num_clusters();
+  const long long limit = p.wait_limit;
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < C::kStages; ++s) {
+      mbar_init(full(s), 1);
+      mbar_init(empty(s), 1);
+    }
+    mbar_init(tfull, 1);
+    mbar_init(tfree, 2 * kPairEpiWarps);   // one arrival per epilogue warp of both CTAs
+    mbar_fence_init();
+    const Fp4Prob &q = p.prob[find_prob(p, cid)];
+    prefetch_tmap(&q.pc);
+    prefetch_tmap(&q.qc);
+    prefetch_tmap(&q.ps);
+    prefetch_tmap(&q.qs);
+  }
+  if (warp == 1) {
+    tmem_alloc2(smem_u32(tmem_slot), 512);
+    tmem_relinquish2();
+  }
+  tc_fence_before();
+  cluster_sync();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  pdl_trigger();
+  pdl_wait();
+  // No wait can run out before this: the shortest limit is about a millisecond.
+  if (p.clear_status && blockIdx.x == 0 && threadIdx.x == 0) *p.status = 0;
+
+  if (warp == 0) {
+    if (lane == 0) {
+      // ------------------------------------------------------------ loads (both CTAs)
+      int stage = 0;
+      uint32_t phase = 0;
+      int last_parity[C::kStages];
+#pragma unroll
+      for (int s = 0; s < C::kStages; ++s) last_parity[s] = -1;
+      bool ok = true;
+      for (int tile = cid; ok && tile < p.total_tiles; tile += ncl) {
+        const Fp4Prob &q = p.prob[find_prob(p, tile)];
+        int pt, qt;
+        tile_of(q, tile - q.tile_begin, pt, qt);
+        for (int kb = 0; kb < q.kt; ++kb) {
+          if (!mbar_wait(empty(stage), phase ^ 1u, limit)) {
+            set_status(p.status, kTimeoutBit);
+            ok = false;
+            break;
+          }
+          const uint32_t sp = base + stage * C::kStage, sq = sp + C::kHalf, ss = sq + C::kHalf;
+          const uint32_t fb = full(stage) & kPeerMask;      // the leader's barrier
+          if (leader) {
+            mbar_arrive_expect_tx(full(stage), 2 * C::kStage);
+#pragma unroll
+            for (int s = 0; s < C::kStages; ++s)
+              if (s == stage) last_parity[s] = (int)phase;
+          }
+          tma_load_2sm(sp, &q.pc, kb * 128, pt * 256 + 128 * (int)rank, fb);
+          tma_load_2sm(sq, &q.qc, kb * 128, qt * 256 + 128 * (int)rank, fb);
+          tma_load_3d_2sm(ss, &q.ps, 0, kb * C::kSTiles, pt * 2 + (int)rank, fb);
+          tma_load_3d_2sm(ss + C::kPs, &q.qs, 0, kb * C::kSTiles, qt * 2, fb);
+          if (++stage == C::kStages) {
+            stage = 0;
+            phase ^= 1u;
+          }
+        }
+      }
+      if (leader) {
+        // every load of the pair that was armed must have landed
+#pragma unroll
+        for (int s = 0; s < C::kStages; ++s)
+          if (last_parity[s] >= 0 && !mbar_wait(full(s), (uint32_t)last_parity[s], limit)) set_status(p.status, kTimeoutBit);
+      }
+    }
+  } else if (warp == 1) {
+    if (lane == 0 && leader) {
+      // ------------------------------------------------------------ copies and MMAs (leader)
+      int stage = 0, tl = 0;
+      uint32_t phase = 0;
+      bool ok = true;
+      for (int tile = cid; ok && tile < p.total_tiles; tile += ncl, ++tl) {
+        const Fp4Prob &q = p.prob[find_prob(p, tile)];
+        // the columns that this tile shares with the one before have been drained, and with them all
+        // of the tile before that
+        if (tl > 0 && !mbar_wait(tfree, (uint32_t)(tl - 1) & 1u, limit)) {
+          set_status(p.status, kTimeoutBit);
+          break;
+        }
+        tc_fence_after();
+        const uint32_t d = tmem + ((tl & 1) ? C::kStep : 0);
+        for (int kb = 0; kb < q.kt; ++kb) {
+          if (!mbar_wait(full(stage), phase, limit)) {
+            set_status(p.status, kTimeoutBit);
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t sp = base + stage * C::kStage, sq = sp + C::kHalf, ss = sq + C::kHalf;
+#pragma unroll
+          for (int j = 0; j < C::kSTiles; ++j) {
+            tc_cp2_scales(tmem + C::kPsCol + 4 * j, smem_desc_scales(ss + 512 * j));
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+              tc_cp2_scales(tmem + C::kQsCol + 4 * (2 * j + i), smem_desc_scales(ss + C::kPs + 512 * (C::kSTiles * i + j)));
+          }
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const int j = NV ? k : k >> 1, id = NV ? 0 : 2 * (k & 1);
+            tc_mma2_fp4<NV>(d, smem_desc_sw128(sp + 32 * k, 16, 1024), smem_desc_sw128(sq + 32 * k, 16, 1024),
+                            idesc_fp4(256, 256, NV, id), tmem + C::kPsCol + 4 * j, tmem + C::kQsCol + 8 * j, (kb | k) != 0);
+          }
+          tc_commit2_mc(empty(stage), 0x3);
+          if (++stage == C::kStages) {
+            stage = 0;
+            phase ^= 1u;
+          }
+        }
+        if (ok) tc_commit2_mc(tfull, 0x3);
+      }
+    }
+  } else {
+    // -------------------------------------------------------------- epilogue (both CTAs)
+    const int quarter = warp & 3, half = (warp - 2) >> 2;
+    int tl = 0;
+    for (int tile = cid; tile < p.total_tiles; tile += ncl, ++tl) {
+      const Fp4Prob &q = p.prob[find_prob(p, tile)];
+      int pt, qt;
+      tile_of(q, tile - q.tile_begin, pt, qt);
+      const float g = q.pg ? *q.pg * *q.qg : 1.f;
+      const bool sym = (q.flags & kFp4Sym) && pt != qt;
+      const int64_t row = (int64_t)pt * 256 + 128 * rank + quarter * 32 + lane;
+      const int d = (tl & 1) ? C::kStep : 0;
+      const int shared_c = (tl & 1) ? 0 : C::kStep, rest_c = (tl & 1) ? 64 : 0;   // tile columns
+      if (!mbar_wait(tfull, (uint32_t)tl & 1u, limit)) {
+        set_status(p.status, kTimeoutBit);
+        break;
+      }
+      tc_fence_after();
+#pragma unroll 1
+      for (int i = 0; i < 4; ++i) {
+        const int c = i == 0 ? shared_c + 32 * half : rest_c + 96 * half + 32 * (i - 1);
+        uint32_t r[32];
+        tmem_ld32(tmem + (uint32_t)(d + c) + ((uint32_t)(quarter * 32) << 16), r);
+        tmem_ld_wait();
+        if (i == 0) {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) remote_arrive(mapa(tfree, 0));
+        }
+        float v[32];
+#pragma unroll
+        for (int e = 0; e < 32; ++e) v[e] = g * __uint_as_float(r[e]);
+        store_row<32>(q, row, (int64_t)qt * 256 + c, v, false);
+        if (sym) store_row<32>(q, row, (int64_t)qt * 256 + c, v, true);
+      }
+      tc_fence_before();
+    }
+  }
+  __syncwarp();
+  tc_fence_before();
+  cluster_sync();   // no CTA leaves while its partner may still read its shared memory or signal it
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc2(tmem, 512);
+  }
+}
+
+template <bool NV, int NP>
+cudaError_t launch_pair(const Fp4GemmParams &p, cudaStream_t s) {
+  using C = PairCfg<NV>;
+  static PerDevice pairs;   // pairs that can be resident at once
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.blockDim = dim3(kPairThreads, 1, 1);
+  cfg.dynamicSmemBytes = C::kSmem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 2;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  int most = pairs.get(dev);
+  if (!most) {
+    e = cudaFuncSetAttribute(fp4_pair_kernel<NV, NP>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+    if (e != cudaSuccess) return e;
+    const int sms = device_sms();
+    cfg.numAttrs = 1;
+    cfg.gridDim = dim3(2 * (sms / 2), 1, 1);
+    if (cudaOccupancyMaxActiveClusters(&most, fp4_pair_kernel<NV, NP>, &cfg) != cudaSuccess || most <= 0) {
+      (void)cudaGetLastError();
+      most = sms / 2;
+    }
+    most = most < sms / 2 ? most : sms / 2;
+    pairs.set(dev, most);
+  }
+  cfg.numAttrs = 2;
+  cfg.gridDim = dim3(2 * (p.total_tiles < most ? p.total_tiles : most), 1, 1);
+  e = cudaLaunchKernelEx(&cfg, fp4_pair_kernel<NV, NP>, prefix<Fp4GemmBlock<NP>>(p));
+  return e != cudaSuccess ? e : cudaGetLastError();
+}
+
 template <int BN, bool NV, bool SPLIT, int NP>
 cudaError_t launch(const Fp4GemmParams &p, int split, cudaStream_t s) {
   using C = Cfg<BN, NV>;
@@ -358,6 +597,9 @@ cudaError_t launch_bn(const Fp4GemmParams &p, int split, cudaStream_t s) {
 cudaError_t launch_fp4_gemm(const Fp4GemmParams &p, int bn, int split, bool nv, cudaStream_t s) {
   if (p.total_tiles <= 0) return cudaSuccess;
   switch (bn) {
+    case 256:
+      if (p.nprob <= kFewFp4Prob) return nv ? launch_pair<true, kFewFp4Prob>(p, s) : launch_pair<false, kFewFp4Prob>(p, s);
+      return nv ? launch_pair<true, kMaxFp4Prob>(p, s) : launch_pair<false, kMaxFp4Prob>(p, s);
     case 16: return nv ? launch_bn<16, true>(p, split, s) : launch_bn<16, false>(p, split, s);
     case 32: return nv ? launch_bn<32, true>(p, split, s) : launch_bn<32, false>(p, split, s);
     case 64: return nv ? launch_bn<64, true>(p, split, s) : launch_bn<64, false>(p, split, s);

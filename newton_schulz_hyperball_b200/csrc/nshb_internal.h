@@ -504,8 +504,9 @@ cudaError_t launch_tens_finalize(const TensFinParams &p, cudaStream_t s);
 cudaError_t launch_tens_scale(const TensParams &p, cudaStream_t s);
 cudaError_t launch_fp4_quantize(const Fp4Params &p, bool transpose, cudaStream_t s);
 cudaError_t launch_fp4_dequantize(const Fp4Params &p, cudaStream_t s);
-// bn: Q rows of a tile (16, 32, 64, 128 or 256; below 128 only with one tile along Q); split: CTAs of a
-// cluster that share a tile's columns (1, 2, 4 or 8).
+// bn: Q rows of a tile: 16, 32, 64 or 128 (below 128 only with one tile along Q) on single CTAs with 128 rows of
+// P, `split` CTAs of a cluster sharing a tile's columns (1, 2, 4 or 8); or 256 on CTA pairs with
+// 256 rows of P (split 1, kt > 0, kFp4DTrans unset).
 cudaError_t launch_fp4_gemm(const Fp4GemmParams &p, int bn, int split, bool nv, cudaStream_t s);
 // Tensor maps of a 4-bit matrix for the products: `rows` rows a box, `srows` row tiles of scales a box.
 cudaError_t encode_fp4_maps(CUtensorMap *codes, CUtensorMap *scales, const nshb_fp4 &q, int rows, int srows);

@@ -100,6 +100,29 @@ def test_gram(fmt, size):
 
 
 @pytest.mark.parametrize("fmt", [MX, NV])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("size", [(2304, 2304, 64), (2300, 2310, 256), (4100, 1300, 1000), (1300, 4100, 1537), (19000, 200, 333)])
+def test_products_of_many_tiles(fmt, dtype, size):
+    test_products(fmt, dtype, size)
+
+
+@pytest.mark.parametrize("fmt", [MX, NV])
+@pytest.mark.parametrize("d,k", [(3000, 700), (3333, 256)])
+def test_gram_of_many_tiles(fmt, d, k):
+    test_gram(fmt, (d, k))
+
+
+@pytest.mark.parametrize("fmt", [MX, NV])
+def test_a_list_of_many_tiles(fmt):
+    shapes = [(1500, 700, 300), (257, 300, 4000), (5, 600, 100), (1000, 1000, 70), (300, 300, 0), (1500, 900, 513)] * 2
+    a = [operand(m, k, fmt, 10 + i) for i, (m, n, k) in enumerate(shapes)]
+    b = [operand(n, k, fmt, 90 + i) for i, (m, n, k) in enumerate(shapes)]
+    ds = product([x[0] for x in a], [x[0] for x in b], torch.float32)
+    for d, x, y, (m, n, k) in zip(ds, a, b, shapes):
+        check(d, x[1], y[1], k)
+
+
+@pytest.mark.parametrize("fmt", [MX, NV])
 def test_a_list(fmt):
     shapes = [(5, 300, 70), (7, 200, 500), (0, 4, 64), (300, 300, 64), (3, 4, 0), (1, 2, 3), (200, 0, 9), (150, 150, 300)] * 7
     a = [operand(m, k, fmt, 10 + i) for i, (m, n, k) in enumerate(shapes)]
