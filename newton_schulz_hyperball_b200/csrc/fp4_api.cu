@@ -64,12 +64,20 @@ struct Shape {
   int64_t tiles;
 };
 
+// Tiles of bm x bn of a p x q result; of a symmetric one those that reach the diagonal or lie below it.
+int64_t count_tiles(int64_t p, int64_t q, int bm, int bn, bool sym) {
+  const int64_t pt = (p + bm - 1) / bm, qt = (q + bn - 1) / bn;
+  if (!sym) return pt * qt;
+  int64_t n = 0;
+  for (int64_t i = 0; i < pt; ++i) n += std::min(qt, (i * bm + bm - 1) / bn + 1);
+  return n;
+}
+
 Shape shape_of(int64_t m, int64_t n, int64_t kt, bool sym, bool pairs) {
   Shape s = {128, 1, false, 0};
   if (pairs && kt > 0 && std::min(m, n) > 128) {
-    const int64_t pt = (m + 255) / 256, qt = (n + 255) / 256;
-    s.bn = 256;
-    s.tiles = sym ? pt * (pt + 1) / 2 : pt * qt;
+    s.bn = kFp4PairBn;
+    s.tiles = count_tiles(m, n, 256, kFp4PairBn, sym);
     return s;
   }
   int64_t p = m, q = n;
@@ -78,8 +86,7 @@ Shape shape_of(int64_t m, int64_t n, int64_t kt, bool sym, bool pairs) {
     if (s.swap) std::swap(p, q);
     s.bn = q <= 16 ? 16 : q <= 32 ? 32 : 64;
   }
-  const int64_t pt = (p + 127) / 128, qt = (q + s.bn - 1) / s.bn;
-  s.tiles = sym ? pt * (pt + 1) / 2 : pt * qt;
+  s.tiles = count_tiles(p, q, 128, s.bn, sym);
   while (s.split < 8 && s.split * 2 <= kt && s.tiles * s.split * 2 <= 2 * device_sms()) s.split *= 2;
   return s;
 }
@@ -104,11 +111,11 @@ nshb_status check_products(const nshb_fp4 *A, const nshb_fp4 *B, const nshb_tens
 // Products of one launch; `d` as the caller stores it.  See launch_fp4_gemm for what the launches share.
 nshb_status run_fp4_products(const nshb_fp4 *A, const nshb_fp4 *B, const nshb_tensor *D, int32_t n, uint32_t *status,
                              bool clear, long long limit, cudaStream_t st) {
-  int64_t wide = 0;   // 256 x 256 tiles of the call
+  int64_t wide = 0;   // tiles of CTA pairs in the call
   for (int32_t i = 0; i < n; ++i)
     if (D[i].rows && D[i].cols) {
       const Shape s = shape_of(D[i].rows, D[i].cols, (A[i].cols + 255) / 256, !B, true);
-      wide += s.bn == 256 ? s.tiles : 0;
+      wide += s.bn == kFp4PairBn ? s.tiles : 0;
     }
   const bool pairs = wide >= device_sms() / 2;
   int32_t i = 0;
@@ -138,13 +145,17 @@ nshb_status run_fp4_products(const nshb_fp4 *A, const nshb_fp4 *B, const nshb_te
       std::memset(&q, 0, sizeof(q));
       const nshb_fp4 &P = s.swap ? b : a, &Q = s.swap ? a : b;
       if (kt) {
-        cudaError_t e = encode_fp4_maps(&q.pc, &q.ps, P, 128, 1);
-        if (e == cudaSuccess)
-          e = s.bn == 256 ? encode_fp4_maps(&q.qc, &q.qs, Q, 128, 2) : encode_fp4_maps(&q.qc, &q.qs, Q, s.bn, 1);
+        cudaError_t e = encode_fp4_maps(&q.pc, &q.ps, P, 128);
+        if (e == cudaSuccess) e = encode_fp4_maps(&q.qc, &q.qs, Q, s.bn == kFp4PairBn ? kFp4PairBn / 2 : s.bn);
         if (e != cudaSuccess) {
           record_cuda_error(e);
           return NSHB_ERR_CUDA;
         }
+        q.psc = static_cast<const uint8_t *>(P.scales);
+        q.qsc = static_cast<const uint8_t *>(Q.scales);
+        q.prt = (int32_t)((P.rows + 127) / 128);
+        q.qrt = (int32_t)((Q.rows + 127) / 128);
+        q.stiles = (int32_t)((a.cols + 127) / 128 * (a.format == NSHB_NVFP4 ? 2 : 1));
         if (a.format == NSHB_NVFP4) {
           q.pg = P.global;
           q.qg = Q.global;

@@ -59,13 +59,16 @@ __device__ __forceinline__ int find_prob(const P &p, int tile) {
   return lo;
 }
 
-// Tile l of a problem: its P and Q tile (all, or those on and below the diagonal).
+// Tile l of a problem: its P and Q tile; of a symmetric result those that reach the diagonal or lie below it.
+template <int BM, int BN>
 __device__ __forceinline__ void tile_of(const Fp4Prob &q, int l, int &pt, int &qt) {
   if (q.flags & kFp4Sym) {
-    pt = (int)((sqrtf(8.f * (float)l + 1.f) - 1.f) * 0.5f);
-    while (pt * (pt + 1) / 2 > l) --pt;
-    while ((pt + 1) * (pt + 2) / 2 <= l) ++pt;
-    qt = l - pt * (pt + 1) / 2;
+    for (pt = 0;; ++pt) {
+      const int n = min(q.qtiles, (pt * BM + BM - 1) / BN + 1);
+      if (l < n) break;
+      l -= n;
+    }
+    qt = l;
   } else {
     pt = l / q.qtiles;
     qt = l - pt * q.qtiles;
@@ -110,6 +113,73 @@ __device__ __forceinline__ void store_row(const Fp4Prob &q, int64_t p, int64_t q
   }
 }
 
+// A warp's 32 rows x 32 columns of D (lane l holds row l) through 2 KB of shared memory, so that a store
+// instruction covers whole 64-byte pieces of rows: with a row per lane each of its 32 lines takes the
+// load/store unit a turn of its own, and the warps that feed the tensor core wait behind it.
+__device__ __forceinline__ void store_block(const Fp4Prob &q, uint8_t *stage, int64_t row0, int64_t c, const float (&v)[32]) {
+  const int lane = threadIdx.x & 31;
+  const bool f32 = q.flags & kFp4DF32;
+  const int rows = (int)(q.np - row0 < 32 ? q.np - row0 : 32), cols = (int)(q.nq - c < 32 ? q.nq - c : 32);
+  if (rows <= 0 || cols <= 0) return;
+  const int esz = f32 ? 4 : 2, wide = 64 / esz;      // columns of a pass
+  const int64_t pitch = q.ld * esz;
+  char *d = static_cast<char *>(q.d) + (row0 * q.ld + c) * esz;
+  uint8_t *mine = stage + lane * 64;
+  const int turn = (lane >> 1) & 3;
+#pragma unroll
+  for (int pass = 0; pass < 2; ++pass) {
+    if (pass == 1 && !f32) break;
+    __syncwarp();
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      uint4 w;
+      if (f32)
+        w = make_uint4(__float_as_uint(v[16 * pass + 4 * k]), __float_as_uint(v[16 * pass + 4 * k + 1]),
+                       __float_as_uint(v[16 * pass + 4 * k + 2]), __float_as_uint(v[16 * pass + 4 * k + 3]));
+      else
+        w = make_uint4(pack_bf16(v[8 * k], v[8 * k + 1]), pack_bf16(v[8 * k + 2], v[8 * k + 3]),
+                       pack_bf16(v[8 * k + 4], v[8 * k + 5]), pack_bf16(v[8 * k + 6], v[8 * k + 7]));
+      *reinterpret_cast<uint4 *>(mine + ((k ^ turn) << 4)) = w;
+    }
+    __syncwarp();
+    const int have = cols - pass * wide < wide ? cols - pass * wide : wide;
+    char *dp = d + 64 * pass;
+    if ((q.flags & kFp4DVec) && have == wide) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int r = 8 * i + (lane >> 2), k = lane & 3;
+        const uint4 w = *reinterpret_cast<const uint4 *>(stage + r * 64 + ((k ^ ((r >> 1) & 3)) << 4));
+        if (r < rows) *reinterpret_cast<uint4 *>(dp + r * pitch + 16 * k) = w;
+      }
+    } else if (f32) {
+      // two rows at a time
+      for (int r = lane >> 4; r < rows; r += 2) {
+        const int e = lane & 15;
+        if (e < have)
+          *reinterpret_cast<uint32_t *>(dp + r * pitch + 4 * e) =
+              *reinterpret_cast<const uint32_t *>(stage + r * 64 + (((e >> 2) ^ ((r >> 1) & 3)) << 4) + 4 * (e & 3));
+      }
+    } else {
+      for (int r = 0; r < rows; ++r)
+        if (lane < have)
+          *reinterpret_cast<unsigned short *>(dp + r * pitch + 2 * lane) =
+              *reinterpret_cast<const unsigned short *>(stage + r * 64 + (((lane >> 3) ^ ((r >> 1) & 3)) << 4) + 2 * (lane & 7));
+    }
+  }
+}
+
+// The mirror image of such a block's elements below the diagonal.
+__device__ __forceinline__ void store_mirror(const Fp4Prob &q, int64_t row, int64_t c, const float (&v)[32]) {
+  if (row >= q.np) return;
+#pragma unroll
+  for (int e = 0; e < 32; ++e) {
+    if (c + e >= row || c + e >= q.nq) break;
+    const int64_t at = (c + e) * q.ld + row;
+    if (q.flags & kFp4DF32) static_cast<float *>(q.d)[at] = v[e];
+    else static_cast<__nv_bfloat16 *>(q.d)[at] = __float2bfloat16_rn(v[e]);
+  }
+}
+
 template <int BN, bool NV, bool SPLIT, int NP>
 __global__ void __launch_bounds__(kThreads, 2) fp4_gemm_kernel(const __grid_constant__ Fp4GemmBlock<NP> p) {
   using C = Cfg<BN, NV>;
@@ -129,7 +199,7 @@ __global__ void __launch_bounds__(kThreads, 2) fp4_gemm_kernel(const __grid_cons
   const int tile = (int)blockIdx.x / parts;
   const Fp4Prob &q = p.prob[find_prob(p, tile)];
   int pt, qt;
-  tile_of(q, tile - q.tile_begin, pt, qt);
+  tile_of<128, BN>(q, tile - q.tile_begin, pt, qt);
   const int k0 = (int)((int64_t)part * q.kt / parts), k1 = (int)((int64_t)(part + 1) * q.kt / parts);
   const long long limit = p.wait_limit;
 
@@ -251,7 +321,14 @@ __global__ void __launch_bounds__(kThreads, 2) fp4_gemm_kernel(const __grid_cons
   auto store = [&](int c, float (&v)[N]) {
 #pragma unroll
     for (int e = 0; e < N; ++e) v[e] *= g;
-    store_row<N>(q, (int64_t)pt * 128 + row, (int64_t)qt * BN + c, v, trans);
+    const int64_t at = (int64_t)qt * BN + c;
+    if constexpr (N == 32) {
+      // the ring is free: this CTA's MMAs are done
+      if (!trans) store_block(q, smem + 2048 * quarter, (int64_t)pt * 128 + 32 * quarter, at, v);
+      else store_row<N>(q, (int64_t)pt * 128 + row, at, v, true);
+    } else {
+      store_row<N>(q, (int64_t)pt * 128 + row, at, v, trans);
+    }
     if (sym && pt != qt) store_row<N>(q, (int64_t)pt * 128 + row, (int64_t)qt * BN + c, v, true);
   };
   if (!SPLIT) {
@@ -315,24 +392,36 @@ __global__ void __launch_bounds__(kThreads, 2) fp4_gemm_kernel(const __grid_cons
   }
 }
 
-// 256 x 256 tiles on CTA pairs, persistent.  The accumulator of the next tile starts 192 columns after (or
-// before) that of this one: two of 256 columns and the scales do not fit the 512 of tensor memory.
-// So the epilogue drains the 64 shared columns first and hands them over at once; the next tile's MMAs run
-// beside the rest of it.
+// 256 x 192 tiles on CTA pairs, persistent: two accumulators of 192 columns leave 128 of tensor memory to the
+// scales (with 256 columns the accumulators would have to overlap, and each tile's MMAs would wait for a
+// part of the epilogue before).
+//
+// A stage is 512 columns of codes (56 KB of a CTA), as two steps of 256: the load path has a fixed cost
+// per barrier round trip (see ns_tc2.cu), so fewer, larger stages stream faster.
+//
+// The scales have eight warps of their own, two sets of four that take the steps in turn.  They load them
+// with plain asynchronous copies and put them into tensor memory by tcgen05.st: a tcgen05.cp of
+// 512 bytes holds the tensor pipe for about 70 clocks, and a step would need 6 (MX) or 12 (NV) of them
+// next to 405 clocks of MMAs.  A step's scales are 24 or 48 columns: 4 a tile for this CTA's rows of P, 8 for
+// the two row tiles that hold the rows of Q.
 template <bool NV>
 struct PairCfg {
-  static constexpr int kSTiles = NV ? 4 : 2;
-  static constexpr int kHalf = 128 * 128;                    // codes of 128 rows
-  static constexpr int kPs = kSTiles * 512, kQs = 2 * kPs;   // P's own rows, all of Q's
-  static constexpr int kStage = 2 * kHalf + kPs + kQs;       // of one CTA
-  static constexpr int kStages = NV ? 5 : 6;
-  static constexpr int kSmem = kStages * kStage + 1024 + 256;
-  static constexpr int kStep = 192;                          // between the two accumulators
-  static constexpr int kPsCol = 448, kQsCol = kPsCol + 4 * kSTiles;
-  static_assert(kStage % 1024 == 0 && kQsCol + 8 * kSTiles <= 512 && kSmem <= 232448, "fits");
+  static constexpr int kBn = 192;
+  static constexpr int kSTiles = NV ? 4 : 2;                 // scale tiles of a step and row tile
+  static constexpr int kP = 128 * 128, kQ = 96 * 128;        // codes of a step in one CTA: its rows of P, half of Q's
+  static constexpr int kStage = 2 * (kP + kQ);
+  static constexpr int kStages = 3;
+  static constexpr int kRt = kSTiles * 512;                  // scales of a step: P's own rows, Q's two row tiles
+  static constexpr int kStep = 3 * kRt;
+  static constexpr int kAhead = NV ? 3 : 4;                  // steps under way, per set
+  static constexpr int kOut = 8 * 2048;                      // a block of D for each epilogue warp
+  static constexpr int kSmem = kStages * kStage + 2 * kAhead * kStep + kOut + 1024 + 256;
+  static constexpr int kScales = 2 * kBn, kBufs = NV ? 2 : 4, kCols = 12 * kSTiles;
+  static constexpr int kQCol = 4 * kSTiles;                  // Q's columns of a buffer
+  static_assert(kSmem <= 232448 && kScales + kCols * kBufs <= 512 && kBufs % 2 == 0, "fits");
 };
-constexpr int kPairEpiWarps = 8;
-constexpr int kPairThreads = 64 + 32 * kPairEpiWarps;
+constexpr int kPairEpiWarps = 8, kPairScaleWarps = 8;
+constexpr int kPairThreads = 64 + 32 * (kPairEpiWarps + kPairScaleWarps);
 constexpr uint32_t kPeerMask = 0xFEFFFFFFu;                  // clears the CTA-rank bit of a cluster address
 
 template <bool NV, int NP>
@@ -340,12 +429,19 @@ __global__ void __launch_bounds__(kPairThreads, 1) fp4_pair_kernel(const __grid_
   using C = PairCfg<NV>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  uint64_t *bars = reinterpret_cast<uint64_t *>(smem + C::kStages * C::kStage);
-  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + 2 * C::kStages + 2);
+  uint8_t *scale_ring = smem + C::kStages * C::kStage;
+  uint8_t *out = scale_ring + 2 * C::kAhead * C::kStep;
+  uint64_t *bars = reinterpret_cast<uint64_t *>(out + C::kOut);
+  constexpr int kBars = 2 * C::kStages + 2 * C::kBufs + 4;
+  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + kBars);
   const uint32_t base = smem_u32(smem), bar_base = smem_u32(bars);
-  auto full = [&](int s) { return bar_base + 8u * s; };
+  auto full = [&](int s) { return bar_base + 8u * s; };                       // codes of the pair (leader's)
   auto empty = [&](int s) { return bar_base + 8u * (C::kStages + s); };
-  const uint32_t tfull = bar_base + 8u * (2 * C::kStages), tfree = tfull + 8u;
+  const uint32_t after = bar_base + 8u * (2 * C::kStages);
+  auto bfull = [&](int b) { return after + 8u * b; };                         // a buffer of scales in both CTAs (leader's)
+  auto bempty = [&](int b) { return after + 8u * (C::kBufs + b); };
+  auto tfull = [&](int b) { return after + 8u * (2 * C::kBufs + b); };
+  auto tempty = [&](int b) { return after + 8u * (2 * C::kBufs + 2 + b); };   // (leader's)
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = cta_rank();
@@ -357,14 +453,18 @@ __global__ void __launch_bounds__(kPairThreads, 1) fp4_pair_kernel(const __grid_
       mbar_init(full(s), 1);
       mbar_init(empty(s), 1);
     }
-    mbar_init(tfull, 1);
-    mbar_init(tfree, 2 * kPairEpiWarps);   // one arrival per epilogue warp of both CTAs
+    for (int b = 0; b < C::kBufs; ++b) {
+      mbar_init(bfull(b), 8);               // a set's four warps in both CTAs
+      mbar_init(bempty(b), 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(tfull(b), 1);
+      mbar_init(tempty(b), 2 * kPairEpiWarps);
+    }
     mbar_fence_init();
     const Fp4Prob &q = p.prob[find_prob(p, cid)];
     prefetch_tmap(&q.pc);
     prefetch_tmap(&q.qc);
-    prefetch_tmap(&q.ps);
-    prefetch_tmap(&q.qs);
   }
   if (warp == 1) {
     tmem_alloc2(smem_u32(tmem_slot), 512);
@@ -381,7 +481,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) fp4_pair_kernel(const __grid_
 
   if (warp == 0) {
     if (lane == 0) {
-      // ------------------------------------------------------------ loads (both CTAs)
+      // ------------------------------------------------------------ codes (both CTAs)
       int stage = 0;
       uint32_t phase = 0;
       int last_parity[C::kStages];
@@ -391,25 +491,29 @@ __global__ void __launch_bounds__(kPairThreads, 1) fp4_pair_kernel(const __grid_
       for (int tile = cid; ok && tile < p.total_tiles; tile += ncl) {
         const Fp4Prob &q = p.prob[find_prob(p, tile)];
         int pt, qt;
-        tile_of(q, tile - q.tile_begin, pt, qt);
-        for (int kb = 0; kb < q.kt; ++kb) {
+        tile_of<256, C::kBn>(q, tile - q.tile_begin, pt, qt);
+        const int prow = pt * 256 + 128 * (int)rank, qrow = qt * C::kBn + 96 * (int)rank;
+        for (int kb = 0; kb < q.kt; kb += 2) {
           if (!mbar_wait(empty(stage), phase ^ 1u, limit)) {
             set_status(p.status, kTimeoutBit);
             ok = false;
             break;
           }
-          const uint32_t sp = base + stage * C::kStage, sq = sp + C::kHalf, ss = sq + C::kHalf;
+          const bool two = kb + 1 < q.kt;
+          const uint32_t sp = base + stage * C::kStage, sq = sp + 2 * C::kP;
           const uint32_t fb = full(stage) & kPeerMask;      // the leader's barrier
           if (leader) {
-            mbar_arrive_expect_tx(full(stage), 2 * C::kStage);
+            mbar_arrive_expect_tx(full(stage), two ? 2 * C::kStage : C::kStage);
 #pragma unroll
             for (int s = 0; s < C::kStages; ++s)
               if (s == stage) last_parity[s] = (int)phase;
           }
-          tma_load_2sm(sp, &q.pc, kb * 128, pt * 256 + 128 * (int)rank, fb);
-          tma_load_2sm(sq, &q.qc, kb * 128, qt * 256 + 128 * (int)rank, fb);
-          tma_load_3d_2sm(ss, &q.ps, 0, kb * C::kSTiles, pt * 2 + (int)rank, fb);
-          tma_load_3d_2sm(ss + C::kPs, &q.qs, 0, kb * C::kSTiles, qt * 2, fb);
+          tma_load_2sm(sp, &q.pc, kb * 128, prow, fb);
+          tma_load_2sm(sq, &q.qc, kb * 128, qrow, fb);
+          if (two) {
+            tma_load_2sm(sp + C::kP, &q.pc, kb * 128 + 128, prow, fb);
+            tma_load_2sm(sq + C::kQ, &q.qc, kb * 128 + 128, qrow, fb);
+          }
           if (++stage == C::kStages) {
             stage = 0;
             phase ^= 1u;
@@ -425,50 +529,157 @@ __global__ void __launch_bounds__(kPairThreads, 1) fp4_pair_kernel(const __grid_
     }
   } else if (warp == 1) {
     if (lane == 0 && leader) {
-      // ------------------------------------------------------------ copies and MMAs (leader)
-      int stage = 0, tl = 0;
-      uint32_t phase = 0;
+      // ------------------------------------------------------------ MMAs (leader)
+      int stage = 0, tl = 0, buf = 0;
+      uint32_t phase = 0, bphase = 0;
       bool ok = true;
       for (int tile = cid; ok && tile < p.total_tiles; tile += ncl, ++tl) {
         const Fp4Prob &q = p.prob[find_prob(p, tile)];
-        // the columns that this tile shares with the one before have been drained, and with them all
-        // of the tile before that
-        if (tl > 0 && !mbar_wait(tfree, (uint32_t)(tl - 1) & 1u, limit)) {
-          set_status(p.status, kTimeoutBit);
-          break;
-        }
+        int pt, qt;
+        tile_of<256, C::kBn>(q, tile - q.tile_begin, pt, qt);
+        const uint32_t qofs = (uint32_t)((qt * C::kBn % 128) >> 5);   // Q's first row within its row tile, in 32s
+        ok = mbar_wait(tempty(tl & 1), ((uint32_t)(tl >> 1) & 1u) ^ 1u, limit);
+        if (!ok) break;
         tc_fence_after();
-        const uint32_t d = tmem + ((tl & 1) ? C::kStep : 0);
-        for (int kb = 0; kb < q.kt; ++kb) {
-          if (!mbar_wait(full(stage), phase, limit)) {
-            set_status(p.status, kTimeoutBit);
-            ok = false;
-            break;
-          }
-          tc_fence_after();
-          const uint32_t sp = base + stage * C::kStage, sq = sp + C::kHalf, ss = sq + C::kHalf;
+        const uint32_t d = tmem + (uint32_t)((tl & 1) * C::kBn);
+        for (int kb = 0; ok && kb < q.kt; kb += 2) {
+          ok = mbar_wait(full(stage), phase, limit);
+          if (!ok) break;
+          const uint32_t sp = base + stage * C::kStage, sq = sp + 2 * C::kP;
 #pragma unroll
-          for (int j = 0; j < C::kSTiles; ++j) {
-            tc_cp2_scales(tmem + C::kPsCol + 4 * j, smem_desc_scales(ss + 512 * j));
+          for (int h = 0; h < 2; ++h) {
+            if (kb + h >= q.kt) break;
+            ok = mbar_wait(bfull(buf), bphase, limit);
+            if (!ok) break;
+            tc_fence_after();
+            const uint32_t sc = tmem + C::kScales + C::kCols * buf;
 #pragma unroll
-            for (int i = 0; i < 2; ++i)
-              tc_cp2_scales(tmem + C::kQsCol + 4 * (2 * j + i), smem_desc_scales(ss + C::kPs + 512 * (C::kSTiles * i + j)));
+            for (int k = 0; k < 4; ++k) {
+              // 64 columns: 32 bytes inside the swizzled rows; MX: half of a scale word, NV: a whole one
+              const int j = NV ? k : k >> 1, id = NV ? 0 : 2 * (k & 1);
+              tc_mma2_fp4<NV>(d, smem_desc_sw128(sp + h * C::kP + 32 * k, 16, 1024),
+                              smem_desc_sw128(sq + h * C::kQ + 32 * k, 16, 1024), idesc_fp4(256, C::kBn, NV, id),
+                              sc + 4 * j, sc + C::kQCol + 8 * j + qofs, (kb | h | k) != 0);
+            }
+            tc_commit2_mc(bempty(buf), 0x3);
+            if (++buf == C::kBufs) {
+              buf = 0;
+              bphase ^= 1u;
+            }
           }
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const int j = NV ? k : k >> 1, id = NV ? 0 : 2 * (k & 1);
-            tc_mma2_fp4<NV>(d, smem_desc_sw128(sp + 32 * k, 16, 1024), smem_desc_sw128(sq + 32 * k, 16, 1024),
-                            idesc_fp4(256, 256, NV, id), tmem + C::kPsCol + 4 * j, tmem + C::kQsCol + 8 * j, (kb | k) != 0);
-          }
+          if (!ok) break;
           tc_commit2_mc(empty(stage), 0x3);
           if (++stage == C::kStages) {
             stage = 0;
             phase ^= 1u;
           }
         }
-        if (ok) tc_commit2_mc(tfull, 0x3);
+        if (ok) tc_commit2_mc(tfull(tl & 1), 0x3);
       }
+      if (!ok) set_status(p.status, kTimeoutBit);
     }
+  } else if (warp >= 2 + kPairEpiWarps) {
+    // -------------------------------------------------------------- scales (both CTAs)
+    // Lane l of a tile of scales is row l of its 32-lane groups; every warp of a set writes the same to
+    // its own 32 lanes of tensor memory.  Set 0 takes steps 0, 2, ... of this pair's work, set 1 the others.
+    const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+    const int t = ((int)threadIdx.x - 32 * (2 + kPairEpiWarps)) & 127;
+    const int set = ((int)threadIdx.x - 32 * (2 + kPairEpiWarps)) >> 7;
+    constexpr int kParts = (C::kStep / 16 + 127) / 128;      // 16-byte pieces of a thread in a step
+    uint8_t *ring = scale_ring + set * C::kAhead * C::kStep;
+    const uint32_t ring_u = smem_u32(ring);
+    // The step that is loaded next: source of each piece, whether its row tile exists.
+    int n_tile = cid, n_kb = set, n_slot = 0, n_kt = 0, n_stiles = 0;
+    const uint8_t *src[kParts];
+    int tile_j[kParts];                                      // scale tile within the step, or out of reach
+    auto aim = [&]() {
+      while (n_tile < p.total_tiles) {
+        const Fp4Prob &q = p.prob[find_prob(p, n_tile)];
+        n_kt = q.kt;
+        if (n_kb < n_kt) {
+          int pt, qt;
+          tile_of<256, C::kBn>(q, n_tile - q.tile_begin, pt, qt);
+          n_stiles = q.stiles;
+#pragma unroll
+          for (int u = 0; u < kParts; ++u) {
+            const int c = t + 128 * u, i = c / (C::kRt / 16), j = (c >> 5) % C::kSTiles;
+            const int r = i == 0 ? pt * 2 + (int)rank : qt * C::kBn / 128 + i - 1;
+            const bool in = c < C::kStep / 16 && r < (i == 0 ? q.prt : q.qrt);
+            tile_j[u] = in ? j : 1 << 30;
+            src[u] = (i == 0 ? q.psc : q.qsc) + (in ? ((int64_t)r * q.stiles + n_kb * C::kSTiles + j) * 512 + 16 * (c & 31) : 0);
+          }
+          return;
+        }
+        n_kb -= n_kt;       // no step of this tile is left for the set
+        n_tile += ncl;
+      }
+    };
+    aim();
+    auto load_next = [&]() {
+      if (n_tile < p.total_tiles) {
+#pragma unroll
+        for (int u = 0; u < kParts; ++u) {
+          const bool in = tile_j[u] < n_stiles - n_kb * C::kSTiles;
+          if (t + 128 * u < C::kStep / 16) cp_async16(ring_u + n_slot * C::kStep + 16 * (t + 128 * u), src[u], in);
+          if (in) src[u] += 2 * C::kRt;
+        }
+        n_kb += 2;
+        if (n_kb >= n_kt) {
+          n_kb -= n_kt;
+          n_tile += ncl;
+          aim();
+        }
+      }
+      cp_async_commit();
+      n_slot = n_slot + 1 == C::kAhead ? 0 : n_slot + 1;
+    };
+#pragma unroll 1
+    for (int i = 0; i < C::kAhead - 1; ++i) load_next();
+    int slot = 0, buf = set, kb = set;
+    uint32_t bphase = 0;
+    bool ok = true;
+    for (int tile = cid; tile < p.total_tiles; tile += ncl) {
+      const int kt = p.prob[find_prob(p, tile)].kt;
+      for (; kb < kt; kb += 2) {
+        cp_async_wait<C::kAhead - 2>();
+        named_barrier(1 + set, 128);       // this step has arrived; the slot before it is free
+        load_next();
+        const uint8_t *ss = ring + slot * C::kStep + 16 * lane;
+        uint4 w[3][C::kSTiles];
+#pragma unroll
+        for (int j = 0; j < C::kSTiles; ++j)
+#pragma unroll
+          for (int i = 0; i < 3; ++i) w[i][j] = *reinterpret_cast<const uint4 *>(ss + i * C::kRt + 512 * j);
+        ok = ok && mbar_wait_warp(bempty(buf), bphase ^ 1u, limit);
+        if (ok) {             // else the MMA warp gave up; keep to the barriers of the set
+          tc_fence_after();
+          const uint32_t to = tmem + C::kScales + C::kCols * buf + lanes;
+#pragma unroll
+          for (int j = 0; j < C::kSTiles; j += 2) {
+            const uint32_t r[8] = {w[0][j].x, w[0][j].y, w[0][j].z, w[0][j].w, w[0][j + 1].x, w[0][j + 1].y, w[0][j + 1].z, w[0][j + 1].w};
+            tmem_st8(to + 4 * j, r);
+          }
+#pragma unroll
+          for (int j = 0; j < C::kSTiles; ++j) {
+            const uint32_t r[8] = {w[1][j].x, w[1][j].y, w[1][j].z, w[1][j].w, w[2][j].x, w[2][j].y, w[2][j].z, w[2][j].w};
+            tmem_st8(to + C::kQCol + 8 * j, r);
+          }
+          tmem_st_wait();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) remote_arrive_relaxed(mapa(bfull(buf), 0));
+        }
+        buf += 2;
+        if (buf >= C::kBufs) {
+          buf = set;
+          bphase ^= 1u;
+        }
+        slot = slot + 1 == C::kAhead ? 0 : slot + 1;
+      }
+      kb -= kt;
+    }
+    cp_async_wait<0>();
+    if (!ok && lane == 0) set_status(p.status, kTimeoutBit);
   } else {
     // -------------------------------------------------------------- epilogue (both CTAs)
     const int quarter = warp & 3, half = (warp - 2) >> 2;
@@ -476,35 +687,32 @@ __global__ void __launch_bounds__(kPairThreads, 1) fp4_pair_kernel(const __grid_
     for (int tile = cid; tile < p.total_tiles; tile += ncl, ++tl) {
       const Fp4Prob &q = p.prob[find_prob(p, tile)];
       int pt, qt;
-      tile_of(q, tile - q.tile_begin, pt, qt);
+      tile_of<256, C::kBn>(q, tile - q.tile_begin, pt, qt);
       const float g = q.pg ? *q.pg * *q.qg : 1.f;
-      const bool sym = (q.flags & kFp4Sym) && pt != qt;
       const int64_t row = (int64_t)pt * 256 + 128 * rank + quarter * 32 + lane;
-      const int d = (tl & 1) ? C::kStep : 0;
-      const int shared_c = (tl & 1) ? 0 : C::kStep, rest_c = (tl & 1) ? 64 : 0;   // tile columns
-      if (!mbar_wait(tfull, (uint32_t)tl & 1u, limit)) {
+      const uint32_t acc = tmem + (uint32_t)((tl & 1) * C::kBn + 96 * half) + ((uint32_t)(quarter * 32) << 16);
+      if (!mbar_wait_warp(tfull(tl & 1), (uint32_t)(tl >> 1) & 1u, limit)) {
         set_status(p.status, kTimeoutBit);
         break;
       }
       tc_fence_after();
 #pragma unroll 1
-      for (int i = 0; i < 4; ++i) {
-        const int c = i == 0 ? shared_c + 32 * half : rest_c + 96 * half + 32 * (i - 1);
+      for (int i = 0; i < 3; ++i) {
         uint32_t r[32];
-        tmem_ld32(tmem + (uint32_t)(d + c) + ((uint32_t)(quarter * 32) << 16), r);
+        tmem_ld32(acc + 32 * i, r);
         tmem_ld_wait();
-        if (i == 0) {
+        if (i == 2) {
           tc_fence_before();
           __syncwarp();
-          if (lane == 0) remote_arrive(mapa(tfree, 0));
+          if (lane == 0) remote_arrive_relaxed(mapa(tempty(tl & 1), 0));
         }
         float v[32];
 #pragma unroll
         for (int e = 0; e < 32; ++e) v[e] = g * __uint_as_float(r[e]);
-        store_row<32>(q, row, (int64_t)qt * 256 + c, v, false);
-        if (sym) store_row<32>(q, row, (int64_t)qt * 256 + c, v, true);
+        const int64_t c = (int64_t)qt * C::kBn + 96 * half + 32 * i;
+        store_block(q, out + 2048 * (warp - 2), row - lane, c, v);
+        if (q.flags & kFp4Sym) store_mirror(q, row, c, v);
       }
-      tc_fence_before();
     }
   }
   __syncwarp();
@@ -597,7 +805,7 @@ cudaError_t launch_bn(const Fp4GemmParams &p, int split, cudaStream_t s) {
 cudaError_t launch_fp4_gemm(const Fp4GemmParams &p, int bn, int split, bool nv, cudaStream_t s) {
   if (p.total_tiles <= 0) return cudaSuccess;
   switch (bn) {
-    case 256:
+    case 192:
       if (p.nprob <= kFewFp4Prob) return nv ? launch_pair<true, kFewFp4Prob>(p, s) : launch_pair<false, kFewFp4Prob>(p, s);
       return nv ? launch_pair<true, kMaxFp4Prob>(p, s) : launch_pair<false, kMaxFp4Prob>(p, s);
     case 16: return nv ? launch_bn<16, true>(p, split, s) : launch_bn<16, false>(p, split, s);

@@ -139,6 +139,15 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, long lo
   return true;
 }
 
+// The same for a whole warp, with one lane at the barrier: 32 polling lanes of several warps hold up
+// the thread that issues the loads they wait for.
+__device__ __forceinline__ bool mbar_wait_warp(uint32_t bar, uint32_t parity, long long limit) {
+  bool ok = true;
+  if ((threadIdx.x & 31) == 0) ok = mbar_wait(bar, parity, limit);
+  __syncwarp();
+  return __shfl_sync(0xffffffffu, (int)ok, 0) != 0;
+}
+
 // ----------------------------------------------------- bulk async copy (no tensor map)
 // Contiguous global -> shared copy of `bytes` (multiple of 16, both addresses 16-byte
 // aligned), completing `bytes` transactions on mbarrier `bar`.
@@ -147,6 +156,21 @@ __device__ __forceinline__ void bulk_g2s(uint32_t dst, const void *src, uint32_t
       "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
       "l"(src), "r"(bytes), "r"(bar)
       : "memory");
+}
+
+// 16 bytes global -> shared per thread, zeros where !valid (`src` is then not read); the copies of a
+// thread are waited for by groups, oldest first.
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, bool valid) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(valid ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+// Barrier `id` (1 ..) of `threads` threads of the block.
+__device__ __forceinline__ void named_barrier(int id, int threads) {
+  asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
 }
 
 // --------------------------------------------------------------------------- tcgen05
@@ -245,6 +269,12 @@ __device__ __forceinline__ void cluster_sync() {
 }
 __device__ __forceinline__ void remote_arrive(uint32_t cluster_addr) {
   asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
+}
+// The same without release semantics: for hand-overs of tensor memory, which the tcgen05 waits and fences
+// order.  The release of the form above waits for every store and load that the SM has under way
+// (a microsecond beside an epilogue).
+__device__ __forceinline__ void remote_arrive_relaxed(uint32_t cluster_addr) {
+  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
 }
 // Pulls a tensor map (a kernel parameter) into the TMA unit's descriptor cache ahead of its
 // first use, e.g. while the kernel waits for the previous one.
@@ -356,17 +386,18 @@ __device__ __forceinline__ void tc_mma2_fp4(uint32_t d_tmem, uint64_t adesc, uin
         "l"(adesc), "l"(bdesc), "r"(idesc), "r"(sa), "r"(sb), "r"(accumulate)
         : "memory");
 }
-// In both CTAs of the pair, from the same offset of their shared memory to the same columns.
-__device__ __forceinline__ void tc_cp2_scales(uint32_t taddr, uint64_t desc) {
-  asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc) : "memory");
+// Keeps the uses of registers that a tcgen05.ld fills behind the wait for it.
+__device__ __forceinline__ void tmem_ld_done(uint32_t (&r)[32]) {
+#pragma unroll
+  for (int e = 0; e < 32; ++e) asm volatile("" : "+r"(r[e]));
 }
-__device__ __forceinline__ void tma_load_3d_2sm(uint32_t dst, const CUtensorMap *map, int x, int y, int z, uint32_t bar) {
-  asm volatile(
-      "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5}], [%2];" ::
-          "r"(dst),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y), "r"(z)
-      : "memory");
+// 32 lanes x 8 consecutive columns: lane (base + t) gets thread t's registers.
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&r)[8]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(r[0]), "r"(r[1]),
+               "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+               : "memory");
 }
+__device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 // A float of another CTA's shared memory (cluster address).
 __device__ __forceinline__ float ld_cluster(uint32_t addr) {
   float v;
