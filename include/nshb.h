@@ -187,6 +187,16 @@ nshb_status newton_muon_step(const nshb_matrix *mats, int32_t n_mats, const void
                              const int64_t *z_rows, int32_t n_z, int64_t n_tokens,
                              const nshb_params *p, void *ws, size_t ws_bytes, nshb_stream stream);
 
+/* newton_muon_step with its layer inputs in microscaled 4-bit form (see nshb_fp4 below; 0.53 or 0.56 bytes
+ * an element instead of 2): Z[j] is a z_rows x tokens matrix with blocks along the tokens, e.g.
+ * nshb_fp4_quantize with `transpose` of the forward's tokens x features activations.  Z Z^T is formed
+ * from the values that the codes stand for by the 4-bit tensor-core product, the rest is
+ * newton_muon_step.  Z[j].rows (up to 16384) must be a multiple of 64; Z[j].cols is any length > 0, also a
+ * different one for each Z.  Workspace: nshb_workspace_size(..., NSHB_OP_NEWTON_MUON, z_rows, n_z, 64, ...). */
+typedef struct nshb_fp4 nshb_fp4;
+nshb_status newton_muon_step_fp4(const nshb_matrix *mats, int32_t n_mats, const nshb_fp4 *Z, int32_t n_z,
+                                 const nshb_params *p, void *ws, size_t ws_bytes, nshb_stream stream);
+
 /* Muon step followed by the RelativeUpdate hook (PR #224 file list: a pre-update scaling that
  * matches the update's norm to the current weight norm):
  *   W <- (1 - lr wd) W - lr ||W||_F O / max(||O||_F, hb_eps)
@@ -233,6 +243,14 @@ nshb_status nshb_workspace_size_min(const nshb_matrix *mats, int32_t n_mats, con
                                     size_t *bytes);
 nshb_status nshb_step_chunked(int32_t op, const nshb_matrix *mats, int32_t n_mats, const nshb_params *p, void *ws,
                               size_t ws_bytes, nshb_stream stream, int32_t *n_chunks);
+
+/* The step of kind `op` (NSHB_OP_MUON, _HYPERBALL, _RADIAL_BRAKE, _HIMUON or _RELATIVE_UPDATE) with every
+ * gradient multiplied by *factor (a DEVICE scalar, 4-byte aligned) as the momentum pass reads it: gradients
+ * clipped by total[1] of nshb_grad_norm without a pass over them.  The product is formed in
+ * fp32 and not rounded to the gradients' dtype; for fp32 gradients the result is that of
+ * nshb_scale_grads followed by the step, bit for bit. */
+nshb_status nshb_step_scaled(int32_t op, const nshb_matrix *mats, int32_t n_mats, const nshb_params *p,
+                             const float *factor, void *ws, size_t ws_bytes, nshb_stream stream);
 
 /* out[i] = ||W_i||_F (fp32) into the DEVICE array out (n_mats floats, 4-byte aligned, else
  * NSHB_ERR_SHAPE), e.g. rho = ||W0||.
@@ -323,14 +341,14 @@ nshb_status nshb_scale_grads(const nshb_tensor *src, const nshb_tensor *dst, int
  *         tile at byte 16 (r mod 32) + 4 (r div 32) + s: the order in which the tensor core reads them.
  * nshb_fp4_size gives the bytes of both.  rows and cols up to 2^24; 0 allowed (nothing is read or written). */
 typedef enum { NSHB_MXFP4 = 0, NSHB_NVFP4 = 1 } nshb_fp4_format;
-typedef struct {
+struct nshb_fp4 {
   int64_t rows, cols;
   int32_t format;   /* nshb_fp4_format */
   int32_t reserved; /* 0 */
   void *codes;
   void *scales;
   float *global;    /* NSHB_NVFP4 only */
-} nshb_fp4;
+};
 nshb_status nshb_fp4_size(int64_t rows, int64_t cols, int32_t format, size_t *code_bytes, size_t *scale_bytes);
 
 /* Q[i] = the 4-bit form of X[i] (bf16 or fp32), or with `transpose` of its transpose (Q[i] then has X[i]'s

@@ -289,6 +289,34 @@ def newton_muon_step(mats, Z, n_tokens: int, p, ws, stream=None):
                                   _stream(stream)), "newton_muon_step")
 
 
+def newton_muon_step_fp4(mats, Z, p, ws, stream=None):
+    """Newton-Muon step with 4-bit layer inputs; Z an fp4_matrices array of z_rows x tokens matrices, `ws`
+    from workspace(..., NSHB_OP_NEWTON_MUON, z_rows=[rows of each Z], n_tokens=64)."""
+    _check_rho(p, _n(mats))
+    ptr, nbytes = _ws(ws)
+    _on("newton_muon_step_fp4", Z, (("W[0]", _first_weight(mats)), ("workspace", ws)), stream,
+        mats, _n(mats), Z, _n(Z), ctypes.byref(p), ptr, nbytes)
+
+
+def step_scaled(op: int, mats, p, factor, ws, stream=None):
+    """The step of kind `op` with every gradient multiplied by the one-element CUDA float32 tensor `factor`
+    (total[1:] of grad_norm: clipped gradients) as it is read."""
+    import torch
+    _device_arg(factor, "factor", torch.float32, 1)
+    w = _first_weight(mats)
+    if w is not None and not isinstance(factor, int) and factor.device != w.device:
+        raise ValueError(f"factor is on {factor.device}, the matrices on {w.device}")
+    _check_rho(p, _n(mats))
+    ptr, nbytes = _ws(ws)
+    _check(lib().nshb_step_scaled(op, mats, _n(mats), ctypes.byref(p), _ptr(factor), ptr, nbytes, _stream(stream)),
+           "nshb_step_scaled")
+
+
+def _first_weight(mats):
+    W = getattr(mats, "_keep", ((),))[0]
+    return W[0] if len(W) else None
+
+
 def fro_norms(mats, out, ws, stream=None):
     import torch
     _device_arg(out, "out", torch.float32, _n(mats))

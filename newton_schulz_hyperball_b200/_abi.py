@@ -142,6 +142,9 @@ SIGNATURES = {
                                                  ctypes.POINTER(ctypes.c_size_t)]),
     "nshb_step_chunked": (ctypes.c_int32, [ctypes.c_int32, _MATS, ctypes.c_int32, _PAR, _P, ctypes.c_size_t, _P,
                                            ctypes.POINTER(ctypes.c_int32)]),
+    "nshb_step_scaled": (ctypes.c_int32, [ctypes.c_int32, _MATS, ctypes.c_int32, _PAR, _P, _P, ctypes.c_size_t, _P]),
+    "newton_muon_step_fp4": (ctypes.c_int32, [_MATS, ctypes.c_int32, _FP4, ctypes.c_int32, _PAR, _P, ctypes.c_size_t,
+                                              _P]),
     "nshb_fro_norms": (ctypes.c_int32, [_MATS, ctypes.c_int32, _P, _P, ctypes.c_size_t, _P]),
     "nshb_fro_norms_static": (ctypes.c_int32, [_MATS, ctypes.c_int32, _P, _P]),
     "nshb_tensor_workspace_size": (ctypes.c_int32, [_TENS, ctypes.c_int32, ctypes.POINTER(ctypes.c_size_t)]),

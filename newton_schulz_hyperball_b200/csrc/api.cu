@@ -15,6 +15,7 @@
 
 #include "../../include/nshb.h"
 #include "nshb_internal.h"
+#include "tensor_lists.h"
 
 namespace nshb {
 
@@ -402,7 +403,7 @@ struct ProfScope {
 
 // momentum + per-segment norms
 nshb_status run_momentum(const nshb_matrix *mats, const Plan &pl, const nshb_params *p, char *ws,
-                         cudaStream_t st, bool from_p = false) {
+                         cudaStream_t st, bool from_p = false, const float *factor = nullptr) {
   const int n = (int)pl.mp.size();
   double *k1part = reinterpret_cast<double *>(ws + pl.k1part_off);
   for (int c0 = 0; c0 < n; c0 += kMaxMats) {
@@ -412,6 +413,7 @@ nshb_status run_momentum(const nshb_matrix *mats, const Plan &pl, const nshb_par
     mp.ws = ws;
     mp.partials = k1part + kK1PartsPerBlock * (int64_t)pl.mp[c0].k1_begin;
     mp.status = reinterpret_cast<uint32_t *>(ws);
+    mp.factor = factor;
     mp.beta = p->beta;
     mp.nesterov = p->nesterov ? 1 : 0;
     mp.nmat = c1 - c0;
@@ -802,7 +804,7 @@ nshb_status run_split(const std::vector<SplitItem> &items, char *ws, cudaStream_
 
 // P = U (Z Z^T + lambda I)^-1 for every matrix; leaves P (fp32, m x n) at pl.r_off[i].
 nshb_status run_newton_precond(const nshb_matrix *mats, const Plan &pl, const nshb_params *p, char *ws,
-                               cudaStream_t st) {
+                               cudaStream_t st, const nshb_fp4 *Zq = nullptr) {
   const int n = (int)pl.mp.size(), nz = (int)pl.zp.size();
   uint32_t *status = reinterpret_cast<uint32_t *>(ws);
   const long long limit = (p->debug_flags & 1u) ? kWaitLimitTest : kWaitLimit;
@@ -828,8 +830,15 @@ nshb_status run_newton_precond(const nshb_matrix *mats, const Plan &pl, const ns
     mp.total_blocks = nb;
     NSHB_LAUNCH(NSHB_PROF_MOMENTUM, launch_momentum(mp, st));
   }
-  // 2. S = Z Z^T on the tensor cores (fp32 out), its operands read straight from each Z
-  for (int c0 = 0; c0 < nz; c0 += kMaxZMaps) {
+  // 2. S = Z Z^T on the tensor cores (fp32 out), its operands read straight from each Z (4-bit: both
+  //    triangles, zeros in the padding like the other)
+  if (Zq) {
+    nshb_tensor S[kMaxMats];
+    for (int j = 0; j < nz; ++j) S[j] = {pl.zp[j].Dp, pl.zp[j].Dp, pl.zp[j].Dp, NSHB_F32, 0, ws + pl.zp[j].s};
+    const nshb_status e = run_fp4_products(Zq, nullptr, S, nz, status, /*clear=*/false, limit, st);
+    if (e != NSHB_OK) return e;
+  }
+  for (int c0 = 0; !Zq && c0 < nz; c0 += kMaxZMaps) {
     const int c1 = std::min(nz, c0 + kMaxZMaps);
     SyrkParams gp;
     std::memset(&gp, 0, sizeof(gp));
@@ -1180,7 +1189,7 @@ nshb_status check_ws(const Plan &pl, void *ws, size_t ws_bytes) {
 // keep_status: a later chunk of one chunked call, which adds its flags to the status word
 // the earlier chunks set (only the exact-pass counter starts again from zero).
 nshb_status do_step(const nshb_matrix *mats, int n_mats, const nshb_params *p, int op, void *ws, size_t ws_bytes,
-                    cudaStream_t st, bool keep_status = false) {
+                    cudaStream_t st, bool keep_status = false, const float *factor = nullptr) {
   Plan pl;
   nshb_status e = plan_step(mats, n_mats, p, op, pl);
   if (e != NSHB_OK) return e;
@@ -1192,7 +1201,7 @@ nshb_status do_step(const nshb_matrix *mats, int n_mats, const nshb_params *p, i
     NSHB_CHECK_CUDA(cudaMemsetAsync(w + sizeof(uint32_t), 0, sizeof(uint32_t), st));  // exact-pass counter
   else
     NSHB_CHECK_CUDA(cudaMemsetAsync(w, 0, 2 * sizeof(uint32_t), st));  // status word, exact-pass counter
-  e = run_momentum(mats, pl, p, w, st);
+  e = run_momentum(mats, pl, p, w, st, /*from_p=*/false, factor);
   if (e != NSHB_OK) return e;
   std::vector<int64_t> o_off;
   e = run_ns(mats, pl, p, w, st, o_off);
@@ -1202,6 +1211,20 @@ nshb_status do_step(const nshb_matrix *mats, int n_mats, const nshb_params *p, i
                   : op == NSHB_OP_RELATIVE_UPDATE ? kOpRelative
                                                   : kOpHyperball;
   return run_apply(mats, pl, p, aop, w, st, o_off, nullptr);
+}
+
+// The launches of a planned Newton-Muon step.
+nshb_status run_newton(const nshb_matrix *mats, const Plan &pl, const nshb_params *p, char *w, cudaStream_t st,
+                       const nshb_fp4 *Zq) {
+  NSHB_CHECK_CUDA(cudaMemsetAsync(w, 0, 2 * sizeof(uint32_t), st));  // status word, exact-pass counter
+  nshb_status e = run_newton_precond(mats, pl, p, w, st, Zq);
+  if (e != NSHB_OK) return e;
+  e = run_momentum(mats, pl, p, w, st, /*from_p=*/true);
+  if (e != NSHB_OK) return e;
+  std::vector<int64_t> o_off;
+  e = run_ns(mats, pl, p, w, st, o_off);
+  if (e != NSHB_OK) return e;
+  return run_apply(mats, pl, p, kOpHyperball, w, st, o_off, nullptr);
 }
 
 // AdamH: no NS.  Per matrix the Adam direction U~ in the layout the apply kernels read as O
@@ -1461,17 +1484,29 @@ nshb_status newton_muon_step(const nshb_matrix *mats, int32_t n_mats, const void
   if (e != NSHB_OK) return e;
   e = check_ws(pl, ws, ws_bytes);
   if (e != NSHB_OK) return e;
-  char *w = static_cast<char *>(ws);
-  cudaStream_t st = (cudaStream_t)stream;
-  NSHB_CHECK_CUDA(cudaMemsetAsync(w, 0, 2 * sizeof(uint32_t), st));  // status word, exact-pass counter
-  e = run_newton_precond(mats, pl, p, w, st);
+  return run_newton(mats, pl, p, static_cast<char *>(ws), (cudaStream_t)stream, nullptr);
+}
+
+nshb_status newton_muon_step_fp4(const nshb_matrix *mats, int32_t n_mats, const nshb_fp4 *Z, int32_t n_z,
+                                 const nshb_params *p, void *ws, size_t ws_bytes, nshb_stream stream) {
+  Plan pl;
+  nshb_status e = plan_step(mats, n_mats, p, NSHB_OP_NEWTON_MUON, pl);
   if (e != NSHB_OK) return e;
-  e = run_momentum(mats, pl, p, w, st, /*from_p=*/true);
+  if (n_mats == 0) return NSHB_OK;
+  if (!Z || n_z <= 0) return NSHB_ERR_NULL;
+  if (n_z > kMaxMats) return NSHB_ERR_UNSUPPORTED;
+  int64_t rows[kMaxMats];
+  for (int32_t j = 0; j < n_z; ++j) {
+    e = check_fp4(Z[j]);
+    if (e != NSHB_OK) return e;
+    if (Z[j].cols == 0) return NSHB_ERR_SHAPE;
+    rows[j] = Z[j].rows;
+  }
+  e = plan_newton(mats, n_mats, nullptr, rows, n_z, 64, pl);
   if (e != NSHB_OK) return e;
-  std::vector<int64_t> o_off;
-  e = run_ns(mats, pl, p, w, st, o_off);
+  e = check_ws(pl, ws, ws_bytes);
   if (e != NSHB_OK) return e;
-  return run_apply(mats, pl, p, kOpHyperball, w, st, o_off, nullptr);
+  return run_newton(mats, pl, p, static_cast<char *>(ws), (cudaStream_t)stream, Z);
 }
 
 static bool chunkable_op(int32_t op) {
@@ -1540,6 +1575,14 @@ nshb_status nshb_step_chunked(int32_t op, const nshb_matrix *mats, int32_t n_mat
     if (e != NSHB_OK) return e;
   }
   return NSHB_OK;
+}
+
+nshb_status nshb_step_scaled(int32_t op, const nshb_matrix *mats, int32_t n_mats, const nshb_params *p,
+                             const float *factor, void *ws, size_t ws_bytes, nshb_stream stream) {
+  if (!chunkable_op(op)) return NSHB_ERR_PARAM;
+  if (!factor) return NSHB_ERR_NULL;
+  if ((uintptr_t)factor % sizeof(float)) return NSHB_ERR_SHAPE;
+  return do_step(mats, n_mats, p, op, ws, ws_bytes, (cudaStream_t)stream, /*keep_status=*/false, factor);
 }
 
 nshb_status nshb_fro_norms(const nshb_matrix *mats, int32_t n_mats, float *out, void *ws, size_t ws_bytes,

@@ -71,6 +71,7 @@ struct MomentumParams {
   char *ws;
   double *partials;  // kK1PartsPerBlock per block of the launch
   uint32_t *status;
+  const float *factor;   // device scalar that multiplies every gradient, or NULL
   float beta;
   int32_t nesterov;
   int32_t nmat, total_blocks;

@@ -275,7 +275,7 @@ __device__ __forceinline__ void momentum_load(const MomentumParams &p, const Mat
 // One 64x64 block: momentum update, U into the NS operand storage, ||U||^2 partial.
 template <bool F32>
 __device__ __forceinline__ void momentum_block(const MomentumParams &p, const MatDesc &d, int cblk, int cr0,
-                                               int cc0, const MomIn &in, float (&sT)[2][kBlk][kBlk + 1]) {
+                                               int cc0, const MomIn &in, float factor, float (&sT)[2][kBlk][kBlk + 1]) {
   const int rq = threadIdx.x >> 3, cq = (threadIdx.x & 7) * 8;
   const bool f32 = F32 && (d.flags & kWF32), vec = d.flags & kVec;
   const bool from_p = F32 && (d.flags & kFromP);
@@ -303,9 +303,10 @@ __device__ __forceinline__ void momentum_block(const MomentumParams &p, const Ma
       if (from_p) {
         uf = g[e];
       } else {
-        const float mnew = fmaf(beta, mm[e], omb * g[e]);
+        const float gs = factor * g[e];
+        const float mnew = fmaf(beta, mm[e], omb * gs);
         mm[e] = mnew;
-        uf = p.nesterov ? fmaf(omb, g[e], beta * mnew) : mnew;
+        uf = p.nesterov ? fmaf(omb, gs, beta * mnew) : mnew;
       }
       if (!full && !(i < d.m && j + e < d.n)) uf = 0.f;
       const float uh = round_bf16 ? bf16_round(uf) : uf;
@@ -365,6 +366,7 @@ __global__ void __launch_bounds__(kThreads, 2) momentum_kernel(const __grid_cons
   __shared__ float sT[2][kBlk][kBlk + 1];   // transpose staging (tall matrices): hi, lo
   int blk = blockIdx.x;
   if (blk >= p.total_blocks) return;
+  const float factor = p.factor ? *p.factor : 1.f;
   int mi = find_mat(p, blk);
   int r0, c0;
   block_origin(p.mats[mi], blk - p.mats[mi].blk_begin, r0, c0);
@@ -398,7 +400,7 @@ __global__ void __launch_bounds__(kThreads, 2) momentum_kernel(const __grid_cons
       block_origin(p.mats[mi2], blk2 - p.mats[mi2].blk_begin, r2, c2);
       momentum_load<F32>(p, p.mats[mi2], r2, c2, n2);
     }
-    momentum_block<F32>(p, d, cblk, cr0, cc0, in, sT);
+    momentum_block<F32>(p, d, cblk, cr0, cc0, in, factor, sT);
     if (blk >= p.total_blocks) break;
   }
 }

@@ -154,6 +154,22 @@ def reduce_scatter_grads(grads, plan: ShardPlan, out, group=None, average: bool 
         off += n
 
 
+def clip_factor(norm, max_norm: float):
+    """min(1, max_norm / (norm + 1e-6)) in fp32, 0 for an infinite norm, NaN for a NaN one: what the library's
+    nshb_grad_norm writes next to the norm."""
+    f = (max_norm / (norm.float() + 1e-6)).clamp(max=1.0)
+    return torch.where(torch.isinf(norm), torch.zeros_like(f), f)
+
+
+def global_grad_norm(local_norm, group=None):
+    """The norm over every rank's owned gradients, from each rank's norm of its own (a tensor of one
+    element): the root of the sum of squares, summed in fp64."""
+    import torch.distributed as dist
+    sq = local_norm.double().square()
+    dist.all_reduce(sq, op=dist.ReduceOp.SUM, group=group)
+    return sq.sqrt().float()
+
+
 def sharded_step(step_fn, weights, plan: ShardPlan, group=None) -> None:
     """Runs `step_fn(local_indices)` (which updates those weights in place) and exchanges
     the results so that every rank ends with all updated weights."""
@@ -169,13 +185,16 @@ class ShardedOptimizer:
     the gradient buffers of the matrices it owns (LPT by NS work), and one step is
 
         reduce-scatter of the ranks' gradients onto the owners (sum, or mean)
+        -> with max_grad_norm: the norm over all gradients (one all-reduce of a scalar)
         -> the library's step ("hyperball", "muon", "brake" or "himuon") on the owned matrices
         -> all-gather of the updated weights.
 
+    max_grad_norm clips the reduced gradients of all ranks together to that norm; the step multiplies them
+    as it reads them.  grad_total then holds the last step's (norm, factor) on the device.
     Keyword arguments go to the library's nshb_params (eta, tile, lr, ...)."""
 
     def __init__(self, weights, rho, plan: ShardPlan, kind: str = "hyperball", group=None, average: bool = True,
-                 **params):
+                 max_grad_norm: float | None = None, **params):
         import newton_schulz_hyperball_b200 as nshb
         self.nshb = nshb
         self.W = weights
@@ -191,6 +210,14 @@ class ShardedOptimizer:
                    "himuon": nshb.himuon_step}[kind]
         op = {"hyperball": nshb.NSHB_OP_HYPERBALL, "muon": nshb.NSHB_OP_MUON, "brake": nshb.NSHB_OP_RADIAL_BRAKE,
               "himuon": nshb.NSHB_OP_HIMUON}[kind]
+        self.op = op
+        self.max_grad_norm = max_grad_norm
+        if max_grad_norm is not None:
+            if not max_grad_norm > 0:
+                raise ValueError("max_grad_norm must be positive")
+            self.grads = nshb.tensors(self.G)
+            self.grad_ws = nshb.tensor_workspace(self.grads) if self.G else None
+            self.grad_total = torch.zeros(2, dtype=torch.float32, device=dev)
         self.mats = None
         if self.local:
             idx = torch.tensor(self.local, dtype=torch.long, device=rho.device)
@@ -204,12 +231,30 @@ class ShardedOptimizer:
     def step(self, grads, stream=None) -> None:
         """One step with this rank's gradients of every matrix (`grads`, in matrix order)."""
         reduce_scatter_grads(grads, self.plan, self.G, self.group, self.average)
+        if self.max_grad_norm is not None:
+            self.measure_grads(stream)
         self.local_step(stream)
         all_gather_weights(self.W, self.plan, self.group)
 
+    def measure_grads(self, stream=None) -> None:
+        """(norm, clip factor) of all ranks' reduced gradients into grad_total."""
+        if isinstance(stream, int):
+            stream = torch.cuda.ExternalStream(stream)
+        with torch.cuda.stream(stream):      # the collective and the factor on the step's stream
+            if self.mats is not None:
+                self.nshb.grad_norm(self.grads, self.grad_total, self.grad_ws, max_norm=self.max_grad_norm)
+            if self.plan.world > 1:
+                norm = global_grad_norm(self.grad_total[:1], self.group)
+                self.grad_total.copy_(torch.cat((norm, clip_factor(norm, self.max_grad_norm))))
+
     def local_step(self, stream=None) -> None:
-        """The library's step on the owned matrices, with the gradients already in self.G."""
-        if self.mats is not None:
+        """The library's step on the owned matrices, with the gradients already in self.G (and with
+        max_grad_norm their norm in grad_total)."""
+        if self.mats is None:
+            return
+        if self.max_grad_norm is not None:
+            self.nshb.step_scaled(self.op, self.mats, self.p, self.grad_total[1:], self.ws, stream)
+        else:
             self.fn(self.mats, self.p, self.ws, stream)
 
     def device_status(self) -> int:

@@ -182,3 +182,40 @@ def test_bad_products():
     assert matmul(a, b, d) == nshb.NSHB_ERR_NULL
     with pytest.raises(ValueError, match="operands"):
         nshb.fp4_matmul(a, fake4((6, 70), (6, 70)), d, (WS, 1 << 20))
+
+
+# --------------------------------------------------------- steps that take them
+
+
+def fake_mats(*shapes):
+    arr = (nshb.nshb_matrix * len(shapes))()
+    for i, (r, c) in enumerate(shapes):
+        arr[i].rows, arr[i].cols, arr[i].ld, arr[i].w_dtype, arr[i].z_index = r, c, c, nshb.NSHB_BF16, 0
+        arr[i].W, arr[i].G, arr[i].M = 0x1000000, 0x2000000, 0x3000000
+    arr._n = len(shapes)
+    return arr
+
+
+def test_scaled_step_refusals():
+    m, p = fake_mats((64, 64)), nshb.params()
+    call = lambda op, f, ws=0x9000000, nb=1 << 30: nshb.lib().nshb_step_scaled(op, m, 1, ctypes.byref(p), f, ws, nb, None)  # noqa: E731
+    for op in (nshb.NSHB_OP_NEWTON_MUON, nshb.NSHB_OP_ADAMH, 99, -1):
+        assert call(op, TOTAL) == nshb.NSHB_ERR_PARAM
+    assert call(nshb.NSHB_OP_MUON, None) == call(nshb.NSHB_OP_MUON, TOTAL, ws=None) == nshb.NSHB_ERR_NULL
+    assert call(nshb.NSHB_OP_MUON, TOTAL + 1) == nshb.NSHB_ERR_SHAPE
+    assert call(nshb.NSHB_OP_MUON, TOTAL, nb=256) == nshb.NSHB_ERR_WORKSPACE
+
+
+def test_newton_step_on_4_bit_inputs_refusals():
+    m, p = fake_mats((100, 128)), nshb.params()
+    call = lambda z, n=1, ws=0x9000000, nb=1 << 32: nshb.lib().newton_muon_step_fp4(m, 1, z, n, ctypes.byref(p), ws, nb, None)  # noqa: E731
+    good = fake4((128, 77))
+    assert call(None) == call(good, n=0) == call(good, ws=None) == nshb.NSHB_ERR_NULL
+    assert call(good, nb=4096) == nshb.NSHB_ERR_WORKSPACE
+    assert call(good, n=300) == nshb.NSHB_ERR_UNSUPPORTED
+    assert call(fake4((128, 0))) == call(fake4((100, 77))) == call(fake4((192, 77))) == nshb.NSHB_ERR_SHAPE
+    bad = fake4((128, 77))
+    bad[0].scales = None
+    assert call(bad) == nshb.NSHB_ERR_NULL
+    m[0].z_index = 1
+    assert call(good) == nshb.NSHB_ERR_PARAM
