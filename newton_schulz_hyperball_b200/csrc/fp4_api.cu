@@ -145,17 +145,13 @@ nshb_status run_fp4_products(const nshb_fp4 *A, const nshb_fp4 *B, const nshb_te
       std::memset(&q, 0, sizeof(q));
       const nshb_fp4 &P = s.swap ? b : a, &Q = s.swap ? a : b;
       if (kt) {
-        cudaError_t e = encode_fp4_maps(&q.pc, &q.ps, P, 128);
-        if (e == cudaSuccess) e = encode_fp4_maps(&q.qc, &q.qs, Q, s.bn == kFp4PairBn ? kFp4PairBn / 2 : s.bn);
+        const bool pair = s.bn == kFp4PairBn;
+        cudaError_t e = encode_fp4_maps(&q.pc, &q.ps, P, 128, pair ? 2 : 1, 1);
+        if (e == cudaSuccess) e = encode_fp4_maps(&q.qc, &q.qs, Q, pair ? kFp4PairBn / 2 : s.bn, pair ? 2 : 1, pair ? 2 : 1);
         if (e != cudaSuccess) {
           record_cuda_error(e);
           return NSHB_ERR_CUDA;
         }
-        q.psc = static_cast<const uint8_t *>(P.scales);
-        q.qsc = static_cast<const uint8_t *>(Q.scales);
-        q.prt = (int32_t)((P.rows + 127) / 128);
-        q.qrt = (int32_t)((Q.rows + 127) / 128);
-        q.stiles = (int32_t)((a.cols + 127) / 128 * (a.format == NSHB_NVFP4 ? 2 : 1));
         if (a.format == NSHB_NVFP4) {
           q.pg = P.global;
           q.qg = Q.global;

@@ -399,29 +399,30 @@ __global__ void __launch_bounds__(kThreads, 2) fp4_gemm_kernel(const __grid_cons
 // A stage is 512 columns of codes (56 KB of a CTA), as two steps of 256: the load path has a fixed cost
 // per barrier round trip (see ns_tc2.cu), so fewer, larger stages stream faster.
 //
-// The scales have eight warps of their own, two sets of four that take the steps in turn.  They load them
-// with plain asynchronous copies and put them into tensor memory by tcgen05.st: a tcgen05.cp of
-// 512 bytes holds the tensor pipe for about 70 clocks, and a step would need 6 (MX) or 12 (NV) of them
-// next to 405 clocks of MMAs.  A step's scales are 24 or 48 columns: 4 a tile for this CTA's rows of P, 8 for
-// the two row tiles that hold the rows of Q.
+// The scales are loaded beside the codes and copied into tensor memory by four warps of their own, whose
+// commits hand the buffers to the MMA warp: one thread starts a tcgen05.cp about every 70 clocks, and a
+// step needs 6 (MX) or 12 (NV) of them next to 405 clocks of MMAs; copies of several warps run at the
+// same time, and beside the MMAs.  (8192 x 6144 x 2048 NVFP4: 83 us with the copies in the MMA warp,
+// 67 us with tcgen05.st from eight warps, which load the shared memory that feeds the MMAs.)  A step's scales
+// are 24 or 48 columns: 4 a tile for this CTA's rows of P, 8 for the two row tiles that hold the rows of Q.
 template <bool NV>
 struct PairCfg {
-  static constexpr int kBn = 192;
+  static constexpr int kBn = kFp4PairBn;
   static constexpr int kSTiles = NV ? 4 : 2;                 // scale tiles of a step and row tile
-  static constexpr int kP = 128 * 128, kQ = 96 * 128;        // codes of a step in one CTA: its rows of P, half of Q's
-  static constexpr int kStage = 2 * (kP + kQ);
+  static constexpr int kP = 128 * 128, kQ = kBn / 2 * 128;   // codes of a step in one CTA: its rows of P, half of Q's
+  static constexpr int kCodes = 2 * (kP + kQ);
+  static constexpr int kRt = 2 * kSTiles * 512;              // scales of a row tile in a stage: P's own, Q's two
+  static constexpr int kStage = kCodes + 3 * kRt;
   static constexpr int kStages = 3;
-  static constexpr int kRt = kSTiles * 512;                  // scales of a step: P's own rows, Q's two row tiles
-  static constexpr int kStep = 3 * kRt;
-  static constexpr int kAhead = NV ? 3 : 4;                  // steps under way, per set
   static constexpr int kOut = 8 * 2048;                      // a block of D for each epilogue warp
-  static constexpr int kSmem = kStages * kStage + 2 * kAhead * kStep + kOut + 1024 + 256;
+  static constexpr int kSmem = kStages * kStage + kOut + 1024 + 256;
   static constexpr int kScales = 2 * kBn, kBufs = NV ? 2 : 4, kCols = 12 * kSTiles;
   static constexpr int kQCol = 4 * kSTiles;                  // Q's columns of a buffer
-  static_assert(kSmem <= 232448 && kScales + kCols * kBufs <= 512 && kBufs % 2 == 0, "fits");
+  static_assert(kStage % 1024 == 0 && kSmem <= 232448 && kScales + kCols * kBufs <= 512, "fits");
 };
-constexpr int kPairEpiWarps = 8, kPairScaleWarps = 8;
-constexpr int kPairThreads = 64 + 32 * (kPairEpiWarps + kPairScaleWarps);
+constexpr int kPairEpiWarps = 8, kPairCopyWarps = 4;
+constexpr int kLoadScalesWarp = 2 + kPairEpiWarps, kFirstCopyWarp = kLoadScalesWarp + 1;
+constexpr int kPairThreads = 32 * (kFirstCopyWarp + kPairCopyWarps);
 constexpr uint32_t kPeerMask = 0xFEFFFFFFu;                  // clears the CTA-rank bit of a cluster address
 
 template <bool NV, int NP>
@@ -429,16 +430,15 @@ __global__ void __launch_bounds__(kPairThreads, 1) fp4_pair_kernel(const __grid_
   using C = PairCfg<NV>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  uint8_t *scale_ring = smem + C::kStages * C::kStage;
-  uint8_t *out = scale_ring + 2 * C::kAhead * C::kStep;
+  uint8_t *out = smem + C::kStages * C::kStage;
   uint64_t *bars = reinterpret_cast<uint64_t *>(out + C::kOut);
   constexpr int kBars = 2 * C::kStages + 2 * C::kBufs + 4;
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + kBars);
   const uint32_t base = smem_u32(smem), bar_base = smem_u32(bars);
-  auto full = [&](int s) { return bar_base + 8u * s; };                       // codes of the pair (leader's)
+  auto full = [&](int s) { return bar_base + 8u * s; };                       // both CTAs' loads (leader's)
   auto empty = [&](int s) { return bar_base + 8u * (C::kStages + s); };
   const uint32_t after = bar_base + 8u * (2 * C::kStages);
-  auto bfull = [&](int b) { return after + 8u * b; };                         // a buffer of scales in both CTAs (leader's)
+  auto bfull = [&](int b) { return after + 8u * b; };                         // a buffer of scales (leader's)
   auto bempty = [&](int b) { return after + 8u * (C::kBufs + b); };
   auto tfull = [&](int b) { return after + 8u * (2 * C::kBufs + b); };
   auto tempty = [&](int b) { return after + 8u * (2 * C::kBufs + 2 + b); };   // (leader's)
@@ -454,7 +454,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) fp4_pair_kernel(const __grid_
       mbar_init(empty(s), 1);
     }
     for (int b = 0; b < C::kBufs; ++b) {
-      mbar_init(bfull(b), 8);               // a set's four warps in both CTAs
+      mbar_init(bfull(b), kPairCopyWarps);
       mbar_init(bempty(b), 1);
     }
     for (int b = 0; b < 2; ++b) {
@@ -465,6 +465,8 @@ __global__ void __launch_bounds__(kPairThreads, 1) fp4_pair_kernel(const __grid_
     const Fp4Prob &q = p.prob[find_prob(p, cid)];
     prefetch_tmap(&q.pc);
     prefetch_tmap(&q.qc);
+    prefetch_tmap(&q.ps);
+    prefetch_tmap(&q.qs);
   }
   if (warp == 1) {
     tmem_alloc2(smem_u32(tmem_slot), 512);
@@ -503,7 +505,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) fp4_pair_kernel(const __grid_
           const uint32_t sp = base + stage * C::kStage, sq = sp + 2 * C::kP;
           const uint32_t fb = full(stage) & kPeerMask;      // the leader's barrier
           if (leader) {
-            mbar_arrive_expect_tx(full(stage), two ? 2 * C::kStage : C::kStage);
+            mbar_arrive_expect_tx(full(stage), 2 * C::kStage - (two ? 0 : C::kCodes));
 #pragma unroll
             for (int s = 0; s < C::kStages; ++s)
               if (s == stage) last_parity[s] = (int)phase;
@@ -561,7 +563,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) fp4_pair_kernel(const __grid_
                               smem_desc_sw128(sq + h * C::kQ + 32 * k, 16, 1024), idesc_fp4(256, C::kBn, NV, id),
                               sc + 4 * j, sc + C::kQCol + 8 * j + qofs, (kb | h | k) != 0);
             }
-            tc_commit2_mc(bempty(buf), 0x3);
+            tc_commit2_mc(bempty(buf), 0x1);
             if (++buf == C::kBufs) {
               buf = 0;
               bphase ^= 1u;
@@ -578,108 +580,70 @@ __global__ void __launch_bounds__(kPairThreads, 1) fp4_pair_kernel(const __grid_
       }
       if (!ok) set_status(p.status, kTimeoutBit);
     }
-  } else if (warp >= 2 + kPairEpiWarps) {
-    // -------------------------------------------------------------- scales (both CTAs)
-    // Lane l of a tile of scales is row l of its 32-lane groups; every warp of a set writes the same to
-    // its own 32 lanes of tensor memory.  Set 0 takes steps 0, 2, ... of this pair's work, set 1 the others.
-    const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
-    const int t = ((int)threadIdx.x - 32 * (2 + kPairEpiWarps)) & 127;
-    const int set = ((int)threadIdx.x - 32 * (2 + kPairEpiWarps)) >> 7;
-    constexpr int kParts = (C::kStep / 16 + 127) / 128;      // 16-byte pieces of a thread in a step
-    uint8_t *ring = scale_ring + set * C::kAhead * C::kStep;
-    const uint32_t ring_u = smem_u32(ring);
-    // The step that is loaded next: source of each piece, whether its row tile exists.
-    int n_tile = cid, n_kb = set, n_slot = 0, n_kt = 0, n_stiles = 0;
-    const uint8_t *src[kParts];
-    int tile_j[kParts];                                      // scale tile within the step, or out of reach
-    auto aim = [&]() {
-      while (n_tile < p.total_tiles) {
-        const Fp4Prob &q = p.prob[find_prob(p, n_tile)];
-        n_kt = q.kt;
-        if (n_kb < n_kt) {
-          int pt, qt;
-          tile_of<256, C::kBn>(q, n_tile - q.tile_begin, pt, qt);
-          n_stiles = q.stiles;
-#pragma unroll
-          for (int u = 0; u < kParts; ++u) {
-            const int c = t + 128 * u, i = c / (C::kRt / 16), j = (c >> 5) % C::kSTiles;
-            const int r = i == 0 ? pt * 2 + (int)rank : qt * C::kBn / 128 + i - 1;
-            const bool in = c < C::kStep / 16 && r < (i == 0 ? q.prt : q.qrt);
-            tile_j[u] = in ? j : 1 << 30;
-            src[u] = (i == 0 ? q.psc : q.qsc) + (in ? ((int64_t)r * q.stiles + n_kb * C::kSTiles + j) * 512 + 16 * (c & 31) : 0);
+  } else if (warp == kLoadScalesWarp) {
+    if (lane == 0) {
+      // ------------------------------------------------------------ scales (both CTAs)
+      int stage = 0;
+      uint32_t phase = 0;
+      bool ok = true;
+      for (int tile = cid; ok && tile < p.total_tiles; tile += ncl) {
+        const Fp4Prob &q = p.prob[find_prob(p, tile)];
+        int pt, qt;
+        tile_of<256, C::kBn>(q, tile - q.tile_begin, pt, qt);
+        for (int kb = 0; kb < q.kt; kb += 2) {
+          ok = mbar_wait(empty(stage), phase ^ 1u, limit);
+          if (!ok) break;               // the warp that loads the codes reports it
+          const uint32_t ss = base + stage * C::kStage + C::kCodes;
+          const uint32_t fb = full(stage) & kPeerMask;
+          tma_load_3d_2sm(ss, &q.ps, 0, kb * C::kSTiles, pt * 2 + (int)rank, fb);
+          tma_load_3d_2sm(ss + C::kRt, &q.qs, 0, kb * C::kSTiles, qt * C::kBn / 128, fb);
+          if (++stage == C::kStages) {
+            stage = 0;
+            phase ^= 1u;
           }
-          return;
-        }
-        n_kb -= n_kt;       // no step of this tile is left for the set
-        n_tile += ncl;
-      }
-    };
-    aim();
-    auto load_next = [&]() {
-      if (n_tile < p.total_tiles) {
-#pragma unroll
-        for (int u = 0; u < kParts; ++u) {
-          const bool in = tile_j[u] < n_stiles - n_kb * C::kSTiles;
-          if (t + 128 * u < C::kStep / 16) cp_async16(ring_u + n_slot * C::kStep + 16 * (t + 128 * u), src[u], in);
-          if (in) src[u] += 2 * C::kRt;
-        }
-        n_kb += 2;
-        if (n_kb >= n_kt) {
-          n_kb -= n_kt;
-          n_tile += ncl;
-          aim();
         }
       }
-      cp_async_commit();
-      n_slot = n_slot + 1 == C::kAhead ? 0 : n_slot + 1;
-    };
-#pragma unroll 1
-    for (int i = 0; i < C::kAhead - 1; ++i) load_next();
-    int slot = 0, buf = set, kb = set;
-    uint32_t bphase = 0;
-    bool ok = true;
-    for (int tile = cid; tile < p.total_tiles; tile += ncl) {
-      const int kt = p.prob[find_prob(p, tile)].kt;
-      for (; kb < kt; kb += 2) {
-        cp_async_wait<C::kAhead - 2>();
-        named_barrier(1 + set, 128);       // this step has arrived; the slot before it is free
-        load_next();
-        const uint8_t *ss = ring + slot * C::kStep + 16 * lane;
-        uint4 w[3][C::kSTiles];
-#pragma unroll
-        for (int j = 0; j < C::kSTiles; ++j)
-#pragma unroll
-          for (int i = 0; i < 3; ++i) w[i][j] = *reinterpret_cast<const uint4 *>(ss + i * C::kRt + 512 * j);
-        ok = ok && mbar_wait_warp(bempty(buf), bphase ^ 1u, limit);
-        if (ok) {             // else the MMA warp gave up; keep to the barriers of the set
-          tc_fence_after();
-          const uint32_t to = tmem + C::kScales + C::kCols * buf + lanes;
-#pragma unroll
-          for (int j = 0; j < C::kSTiles; j += 2) {
-            const uint32_t r[8] = {w[0][j].x, w[0][j].y, w[0][j].z, w[0][j].w, w[0][j + 1].x, w[0][j + 1].y, w[0][j + 1].z, w[0][j + 1].w};
-            tmem_st8(to + 4 * j, r);
-          }
-#pragma unroll
-          for (int j = 0; j < C::kSTiles; ++j) {
-            const uint32_t r[8] = {w[1][j].x, w[1][j].y, w[1][j].z, w[1][j].w, w[2][j].x, w[2][j].y, w[2][j].z, w[2][j].w};
-            tmem_st8(to + C::kQCol + 8 * j, r);
-          }
-          tmem_st_wait();
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) remote_arrive_relaxed(mapa(bfull(buf), 0));
-        }
-        buf += 2;
-        if (buf >= C::kBufs) {
-          buf = set;
-          bphase ^= 1u;
-        }
-        slot = slot + 1 == C::kAhead ? 0 : slot + 1;
-      }
-      kb -= kt;
     }
-    cp_async_wait<0>();
-    if (!ok && lane == 0) set_status(p.status, kTimeoutBit);
+  } else if (warp >= kFirstCopyWarp) {
+    if (lane == 0 && leader) {
+      // ------------------------------------------------------------ scales to tensor memory (leader)
+      const int w = warp - kFirstCopyWarp;
+      int stage = 0, buf = 0;
+      uint32_t phase = 0, bphase = 0;
+      bool ok = true;
+      for (int tile = cid; ok && tile < p.total_tiles; tile += ncl) {
+        const int kt = p.prob[find_prob(p, tile)].kt;
+        for (int kb = 0; ok && kb < kt; kb += 2) {
+          ok = mbar_wait(full(stage), phase, limit);
+          if (!ok) break;
+          const uint32_t ss = base + stage * C::kStage + C::kCodes;
+          for (int h = 0; h < 2 && kb + h < kt; ++h) {
+            ok = mbar_wait(bempty(buf), bphase ^ 1u, limit);
+            if (!ok) break;
+            tc_fence_after();
+            const uint32_t to = tmem + C::kScales + C::kCols * buf;
+            // tile j of row tile i: P's own rows (i = 0), Q's two
+#pragma unroll
+            for (int c = 0; c < 3 * C::kSTiles; ++c) {
+              const int j = c % C::kSTiles, i = c / C::kSTiles;
+              if (c % kPairCopyWarps == w)
+                tc_cp2_scales(to + (i == 0 ? 4 * j : C::kQCol + 8 * j + 4 * (i - 1)),
+                              smem_desc_scales(ss + i * C::kRt + 512 * (C::kSTiles * h + j)));
+            }
+            tc_commit2_mc(bfull(buf), 0x1);
+            if (++buf == C::kBufs) {
+              buf = 0;
+              bphase ^= 1u;
+            }
+          }
+          if (++stage == C::kStages) {
+            stage = 0;
+            phase ^= 1u;
+          }
+        }
+      }
+      if (!ok) set_status(p.status, kTimeoutBit);
+    }
   } else {
     // -------------------------------------------------------------- epilogue (both CTAs)
     const int quarter = warp & 3, half = (warp - 2) >> 2;

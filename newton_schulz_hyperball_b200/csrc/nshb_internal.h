@@ -443,18 +443,14 @@ using Fp4Params = Fp4Block<kMaxFp4>;
 
 // Products of 4-bit matrices (fp4_gemm.cu): D = P Q^T over tiles of P's rows (the accumulator's
 // lanes) x Q's rows (its columns).
-constexpr int kMaxFp4Prob = 48;   // 624 bytes each
+constexpr int kMaxFp4Prob = 48;
 constexpr int kFp4DTrans = 1;    // D element (p, q) goes to d[q * ld + p] (P is the caller's B), else d[p * ld + q]
 constexpr int kFp4DF32 = 2;      // D is fp32 (else bf16)
 constexpr int kFp4Sym = 4;       // P = Q: tiles on and below the diagonal, each also stored mirrored
 constexpr int kFp4DVec = 8;      // D's rows may be accessed 16 bytes at a time
 struct Fp4Prob {
   CUtensorMap pc, qc;            // codes: rows x bytes, 128-byte swizzled boxes of 128 bytes (256 columns)
-  CUtensorMap ps, qs;            // scales: row tiles x column tiles x 512 bytes (single CTAs)
-  const uint8_t *psc, *qsc;      // scales (CTA pairs)
-  int32_t prt, qrt;              // their row tiles
-  int32_t stiles;                // scale tiles of a row tile
-  int32_t pad_;
+  CUtensorMap ps, qs;            // scales: row tiles x column tiles x 512 bytes
   const float *pg, *qg;          // NSHB_NVFP4: the matrices' scales, or NULL
   void *d;
   int64_t ld;
@@ -514,8 +510,10 @@ cudaError_t launch_fp4_dequantize(const Fp4Params &p, cudaStream_t s);
 // 256 rows of P (split 1, kt > 0, kFp4DTrans unset).
 constexpr int kFp4PairBn = 192;
 cudaError_t launch_fp4_gemm(const Fp4GemmParams &p, int bn, int split, bool nv, cudaStream_t s);
-// Tensor maps of a 4-bit matrix for the products: `rows` rows of codes a box, one row tile of scales.
-cudaError_t encode_fp4_maps(CUtensorMap *codes, CUtensorMap *scales, const nshb_fp4 &q, int rows);
+// Tensor maps of a 4-bit matrix for the products: `rows` rows of codes a box; `steps` steps of 256 columns and
+// `row_tiles` row tiles of scales a box.
+cudaError_t encode_fp4_maps(CUtensorMap *codes, CUtensorMap *scales, const nshb_fp4 &q, int rows, int steps,
+                            int row_tiles);
 
 constexpr size_t kMaxParamBytes = 32764;   // kernel parameter limit (CUDA 12.1+, sm_70+)
 static_assert(sizeof(MomentumParams) <= kMaxParamBytes, "MomentumParams");
