@@ -392,32 +392,33 @@ __global__ void __launch_bounds__(kThreads, 2) fp4_gemm_kernel(const __grid_cons
   }
 }
 
-// 256 x 192 tiles on CTA pairs, persistent: two accumulators of 192 columns leave 128 of tensor memory to the
-// scales (with 256 columns the accumulators would have to overlap, and each tile's MMAs would wait for a
-// part of the epilogue before).
+// 256 x 256 tiles on CTA pairs, persistent.  What bounds them is shared memory: a step of 256 columns writes 32 KB of
+// codes and 3 or 6 KB of scales into a CTA's and reads them for 513 clocks of MMAs (narrower tiles move more
+// bytes per MMA: 256 x 192 took 65 us where this takes 45, 8192 x 6144 x 2048 NVFP4).
 //
-// A stage is 512 columns of codes (56 KB of a CTA), as two steps of 256: the load path has a fixed cost
-// per barrier round trip (see ns_tc2.cu), so fewer, larger stages stream faster.
+// Two accumulators of 256 columns and the scales do not fit the 512 columns of tensor memory, so the second
+// accumulator starts 192 (MX) or 160 columns after the first.  The epilogue drains the shared columns
+// first and hands them over; the next tile's MMAs run beside the rest of it.
 //
 // The scales are loaded beside the codes and copied into tensor memory by four warps of their own, whose
 // commits hand the buffers to the MMA warp: one thread starts a tcgen05.cp about every 70 clocks, and a
-// step needs 6 (MX) or 12 (NV) of them next to 405 clocks of MMAs; copies of several warps run at the
-// same time, and beside the MMAs.  (8192 x 6144 x 2048 NVFP4: 83 us with the copies in the MMA warp,
-// 67 us with tcgen05.st from eight warps, which load the shared memory that feeds the MMAs.)  A step's scales
-// are 24 or 48 columns: 4 a tile for this CTA's rows of P, 8 for the two row tiles that hold the rows of Q.
+// step needs 6 (MX) or 12 (NV) of them; copies of several warps run at the same time, and beside the
+// MMAs (83 us with the copies in the MMA warp).  A step's scales are 24 (MX) or 48 columns, a third for this
+// CTA's rows of P, the others for all rows of Q; two buffers.
 template <bool NV>
 struct PairCfg {
   static constexpr int kBn = kFp4PairBn;
   static constexpr int kSTiles = NV ? 4 : 2;                 // scale tiles of a step and row tile
-  static constexpr int kP = 128 * 128, kQ = kBn / 2 * 128;   // codes of a step in one CTA: its rows of P, half of Q's
-  static constexpr int kCodes = 2 * (kP + kQ);
-  static constexpr int kRt = 2 * kSTiles * 512;              // scales of a row tile in a stage: P's own, Q's two
+  static constexpr int kHalf = 128 * 128;                    // codes of 128 rows
+  static constexpr int kCodes = 2 * kHalf;                   // in one CTA: its rows of P, half of Q's
+  static constexpr int kRt = kSTiles * 512;                  // scales of a row tile: P's own, Q's two
   static constexpr int kStage = kCodes + 3 * kRt;
-  static constexpr int kStages = 3;
+  static constexpr int kStages = 5;
   static constexpr int kOut = 8 * 2048;                      // a block of D for each epilogue warp
   static constexpr int kSmem = kStages * kStage + kOut + 1024 + 256;
-  static constexpr int kScales = 2 * kBn, kBufs = NV ? 2 : 4, kCols = 12 * kSTiles;
-  static constexpr int kQCol = 4 * kSTiles;                  // Q's columns of a buffer
+  static constexpr int kCols = 12 * kSTiles, kQCol = 4 * kSTiles, kBufs = 2;   // a step's scales: P's, Q's
+  static constexpr int kShared = NV ? 96 : 64, kShift = 256 - kShared;         // between the accumulators
+  static constexpr int kScales = kShift + 256;
   static_assert(kStage % 1024 == 0 && kSmem <= 232448 && kScales + kCols * kBufs <= 512, "fits");
 };
 constexpr int kPairEpiWarps = 8, kPairCopyWarps = 4;
@@ -432,7 +433,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) fp4_pair_kernel(const __grid_
   uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t *out = smem + C::kStages * C::kStage;
   uint64_t *bars = reinterpret_cast<uint64_t *>(out + C::kOut);
-  constexpr int kBars = 2 * C::kStages + 2 * C::kBufs + 4;
+  constexpr int kBars = 2 * C::kStages + 2 * C::kBufs + 2;
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + kBars);
   const uint32_t base = smem_u32(smem), bar_base = smem_u32(bars);
   auto full = [&](int s) { return bar_base + 8u * s; };                       // both CTAs' loads (leader's)
@@ -440,8 +441,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) fp4_pair_kernel(const __grid_
   const uint32_t after = bar_base + 8u * (2 * C::kStages);
   auto bfull = [&](int b) { return after + 8u * b; };                         // a buffer of scales (leader's)
   auto bempty = [&](int b) { return after + 8u * (C::kBufs + b); };
-  auto tfull = [&](int b) { return after + 8u * (2 * C::kBufs + b); };
-  auto tempty = [&](int b) { return after + 8u * (2 * C::kBufs + 2 + b); };   // (leader's)
+  const uint32_t tfull = after + 8u * (2 * C::kBufs), tfree = tfull + 8u;     // tfree: the leader's
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = cta_rank();
@@ -457,10 +457,8 @@ __global__ void __launch_bounds__(kPairThreads, 1) fp4_pair_kernel(const __grid_
       mbar_init(bfull(b), kPairCopyWarps);
       mbar_init(bempty(b), 1);
     }
-    for (int b = 0; b < 2; ++b) {
-      mbar_init(tfull(b), 1);
-      mbar_init(tempty(b), 2 * kPairEpiWarps);
-    }
+    mbar_init(tfull, 1);
+    mbar_init(tfree, 2 * kPairEpiWarps);   // one arrival per epilogue warp of both CTAs
     mbar_fence_init();
     const Fp4Prob &q = p.prob[find_prob(p, cid)];
     prefetch_tmap(&q.pc);
@@ -493,29 +491,24 @@ __global__ void __launch_bounds__(kPairThreads, 1) fp4_pair_kernel(const __grid_
       for (int tile = cid; ok && tile < p.total_tiles; tile += ncl) {
         const Fp4Prob &q = p.prob[find_prob(p, tile)];
         int pt, qt;
-        tile_of<256, C::kBn>(q, tile - q.tile_begin, pt, qt);
-        const int prow = pt * 256 + 128 * (int)rank, qrow = qt * C::kBn + 96 * (int)rank;
-        for (int kb = 0; kb < q.kt; kb += 2) {
+        tile_of<256, 256>(q, tile - q.tile_begin, pt, qt);
+        const int prow = pt * 256 + 128 * (int)rank, qrow = qt * 256 + 128 * (int)rank;
+        for (int kb = 0; kb < q.kt; ++kb) {
           if (!mbar_wait(empty(stage), phase ^ 1u, limit)) {
             set_status(p.status, kTimeoutBit);
             ok = false;
             break;
           }
-          const bool two = kb + 1 < q.kt;
-          const uint32_t sp = base + stage * C::kStage, sq = sp + 2 * C::kP;
+          const uint32_t sp = base + stage * C::kStage, sq = sp + C::kHalf;
           const uint32_t fb = full(stage) & kPeerMask;      // the leader's barrier
           if (leader) {
-            mbar_arrive_expect_tx(full(stage), 2 * C::kStage - (two ? 0 : C::kCodes));
+            mbar_arrive_expect_tx(full(stage), 2 * C::kStage);
 #pragma unroll
             for (int s = 0; s < C::kStages; ++s)
               if (s == stage) last_parity[s] = (int)phase;
           }
           tma_load_2sm(sp, &q.pc, kb * 128, prow, fb);
           tma_load_2sm(sq, &q.qc, kb * 128, qrow, fb);
-          if (two) {
-            tma_load_2sm(sp + C::kP, &q.pc, kb * 128 + 128, prow, fb);
-            tma_load_2sm(sq + C::kQ, &q.qc, kb * 128 + 128, qrow, fb);
-          }
           if (++stage == C::kStages) {
             stage = 0;
             phase ^= 1u;
@@ -536,47 +529,40 @@ __global__ void __launch_bounds__(kPairThreads, 1) fp4_pair_kernel(const __grid_
       uint32_t phase = 0, bphase = 0;
       bool ok = true;
       for (int tile = cid; ok && tile < p.total_tiles; tile += ncl, ++tl) {
-        const Fp4Prob &q = p.prob[find_prob(p, tile)];
-        int pt, qt;
-        tile_of<256, C::kBn>(q, tile - q.tile_begin, pt, qt);
-        const uint32_t qofs = (uint32_t)((qt * C::kBn % 128) >> 5);   // Q's first row within its row tile, in 32s
-        ok = mbar_wait(tempty(tl & 1), ((uint32_t)(tl >> 1) & 1u) ^ 1u, limit);
+        const int kt = p.prob[find_prob(p, tile)].kt;
+        // the columns that this tile shares with the one before have been drained, and with them all
+        // of the tile before that
+        ok = tl == 0 || mbar_wait(tfree, (uint32_t)(tl - 1) & 1u, limit);
         if (!ok) break;
         tc_fence_after();
-        const uint32_t d = tmem + (uint32_t)((tl & 1) * C::kBn);
-        for (int kb = 0; ok && kb < q.kt; kb += 2) {
+        const uint32_t d = tmem + (uint32_t)((tl & 1) * C::kShift);
+        for (int kb = 0; ok && kb < kt; ++kb) {
           ok = mbar_wait(full(stage), phase, limit);
           if (!ok) break;
-          const uint32_t sp = base + stage * C::kStage, sq = sp + 2 * C::kP;
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            if (kb + h >= q.kt) break;
-            ok = mbar_wait(bfull(buf), bphase, limit);
-            if (!ok) break;
-            tc_fence_after();
-            const uint32_t sc = tmem + C::kScales + C::kCols * buf;
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              // 64 columns: 32 bytes inside the swizzled rows; MX: half of a scale word, NV: a whole one
-              const int j = NV ? k : k >> 1, id = NV ? 0 : 2 * (k & 1);
-              tc_mma2_fp4<NV>(d, smem_desc_sw128(sp + h * C::kP + 32 * k, 16, 1024),
-                              smem_desc_sw128(sq + h * C::kQ + 32 * k, 16, 1024), idesc_fp4(256, C::kBn, NV, id),
-                              sc + 4 * j, sc + C::kQCol + 8 * j + qofs, (kb | h | k) != 0);
-            }
-            tc_commit2_mc(bempty(buf), 0x1);
-            if (++buf == C::kBufs) {
-              buf = 0;
-              bphase ^= 1u;
-            }
-          }
+          const uint32_t sp = base + stage * C::kStage, sq = sp + C::kHalf;
+          ok = mbar_wait(bfull(buf), bphase, limit);
           if (!ok) break;
+          tc_fence_after();
+          const uint32_t sc = tmem + C::kScales + C::kCols * buf;
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            // 64 columns: 32 bytes inside the swizzled rows; MX: half of a scale word, NV: a whole one
+            const int j = NV ? k : k >> 1, id = NV ? 0 : 2 * (k & 1);
+            tc_mma2_fp4<NV>(d, smem_desc_sw128(sp + 32 * k, 16, 1024), smem_desc_sw128(sq + 32 * k, 16, 1024),
+                            idesc_fp4(256, C::kBn, NV, id), sc + 4 * j, sc + C::kQCol + 8 * j, (kb | k) != 0);
+          }
+          tc_commit2_mc(bempty(buf), 0x1);
           tc_commit2_mc(empty(stage), 0x3);
+          if (++buf == C::kBufs) {
+            buf = 0;
+            bphase ^= 1u;
+          }
           if (++stage == C::kStages) {
             stage = 0;
             phase ^= 1u;
           }
         }
-        if (ok) tc_commit2_mc(tfull(tl & 1), 0x3);
+        if (ok) tc_commit2_mc(tfull, 0x3);
       }
       if (!ok) set_status(p.status, kTimeoutBit);
     }
@@ -589,14 +575,14 @@ __global__ void __launch_bounds__(kPairThreads, 1) fp4_pair_kernel(const __grid_
       for (int tile = cid; ok && tile < p.total_tiles; tile += ncl) {
         const Fp4Prob &q = p.prob[find_prob(p, tile)];
         int pt, qt;
-        tile_of<256, C::kBn>(q, tile - q.tile_begin, pt, qt);
-        for (int kb = 0; kb < q.kt; kb += 2) {
+        tile_of<256, 256>(q, tile - q.tile_begin, pt, qt);
+        for (int kb = 0; kb < q.kt; ++kb) {
           ok = mbar_wait(empty(stage), phase ^ 1u, limit);
           if (!ok) break;               // the warp that loads the codes reports it
           const uint32_t ss = base + stage * C::kStage + C::kCodes;
           const uint32_t fb = full(stage) & kPeerMask;
           tma_load_3d_2sm(ss, &q.ps, 0, kb * C::kSTiles, pt * 2 + (int)rank, fb);
-          tma_load_3d_2sm(ss + C::kRt, &q.qs, 0, kb * C::kSTiles, qt * C::kBn / 128, fb);
+          tma_load_3d_2sm(ss + C::kRt, &q.qs, 0, kb * C::kSTiles, qt * 2, fb);
           if (++stage == C::kStages) {
             stage = 0;
             phase ^= 1u;
@@ -613,28 +599,25 @@ __global__ void __launch_bounds__(kPairThreads, 1) fp4_pair_kernel(const __grid_
       bool ok = true;
       for (int tile = cid; ok && tile < p.total_tiles; tile += ncl) {
         const int kt = p.prob[find_prob(p, tile)].kt;
-        for (int kb = 0; ok && kb < kt; kb += 2) {
+        for (int kb = 0; ok && kb < kt; ++kb) {
           ok = mbar_wait(full(stage), phase, limit);
           if (!ok) break;
           const uint32_t ss = base + stage * C::kStage + C::kCodes;
-          for (int h = 0; h < 2 && kb + h < kt; ++h) {
-            ok = mbar_wait(bempty(buf), bphase ^ 1u, limit);
-            if (!ok) break;
-            tc_fence_after();
-            const uint32_t to = tmem + C::kScales + C::kCols * buf;
-            // tile j of row tile i: P's own rows (i = 0), Q's two
+          ok = mbar_wait(bempty(buf), bphase ^ 1u, limit);
+          if (!ok) break;
+          tc_fence_after();
+          const uint32_t to = tmem + C::kScales + C::kCols * buf;
+          // tile j of row tile i: P's own rows (i = 0), Q's two
 #pragma unroll
-            for (int c = 0; c < 3 * C::kSTiles; ++c) {
-              const int j = c % C::kSTiles, i = c / C::kSTiles;
-              if (c % kPairCopyWarps == w)
-                tc_cp2_scales(to + (i == 0 ? 4 * j : C::kQCol + 8 * j + 4 * (i - 1)),
-                              smem_desc_scales(ss + i * C::kRt + 512 * (C::kSTiles * h + j)));
-            }
-            tc_commit2_mc(bfull(buf), 0x1);
-            if (++buf == C::kBufs) {
-              buf = 0;
-              bphase ^= 1u;
-            }
+          for (int c = 0; c < 3 * C::kSTiles; ++c) {
+            const int j = c % C::kSTiles, i = c / C::kSTiles;
+            if (c % kPairCopyWarps == w)
+              tc_cp2_scales(to + (i == 0 ? 4 * j : C::kQCol + 8 * j + 4 * (i - 1)), smem_desc_scales(ss + i * C::kRt + 512 * j));
+          }
+          tc_commit2_mc(bfull(buf), 0x1);
+          if (++buf == C::kBufs) {
+            buf = 0;
+            bphase ^= 1u;
           }
           if (++stage == C::kStages) {
             stage = 0;
@@ -651,32 +634,40 @@ __global__ void __launch_bounds__(kPairThreads, 1) fp4_pair_kernel(const __grid_
     for (int tile = cid; tile < p.total_tiles; tile += ncl, ++tl) {
       const Fp4Prob &q = p.prob[find_prob(p, tile)];
       int pt, qt;
-      tile_of<256, C::kBn>(q, tile - q.tile_begin, pt, qt);
+      tile_of<256, 256>(q, tile - q.tile_begin, pt, qt);
       const float g = q.pg ? *q.pg * *q.qg : 1.f;
       const int64_t row = (int64_t)pt * 256 + 128 * rank + quarter * 32 + lane;
-      const uint32_t acc = tmem + (uint32_t)((tl & 1) * C::kBn + 96 * half) + ((uint32_t)(quarter * 32) << 16);
-      if (!mbar_wait_warp(tfull(tl & 1), (uint32_t)(tl >> 1) & 1u, limit)) {
+      const uint32_t acc = tmem + (uint32_t)((tl & 1) * C::kShift) + ((uint32_t)(quarter * 32) << 16);
+      // 32 columns at a time, the shared ones first: of three such chunks half 0 takes two, of two
+      // each half one
+      constexpr int kChunks = C::kShared / 32;
+      const int shared_c = (tl & 1) ? 0 : C::kShift, rest_c = (tl & 1) ? C::kShared : 0;
+      const int n_shared = kChunks - kChunks / 2 - (half ? kChunks & 1 : 0);
+      const int first_shared = half ? kChunks - kChunks / 2 : 0, first_rest = half ? 4 - (kChunks - kChunks / 2) : 0;
+      if (!mbar_wait_warp(tfull, (uint32_t)tl & 1u, limit)) {
         set_status(p.status, kTimeoutBit);
         break;
       }
       tc_fence_after();
 #pragma unroll 1
-      for (int i = 0; i < 3; ++i) {
+      for (int i = 0; i < 4; ++i) {
+        const int cc = i < n_shared ? shared_c + 32 * (first_shared + i) : rest_c + 32 * (first_rest + i - n_shared);
         uint32_t r[32];
-        tmem_ld32(acc + 32 * i, r);
+        tmem_ld32(acc + cc, r);
         tmem_ld_wait();
-        if (i == 2) {
+        if (i == n_shared - 1) {
           tc_fence_before();
           __syncwarp();
-          if (lane == 0) remote_arrive_relaxed(mapa(tempty(tl & 1), 0));
+          if (lane == 0) remote_arrive_relaxed(mapa(tfree, 0));
         }
         float v[32];
 #pragma unroll
         for (int e = 0; e < 32; ++e) v[e] = g * __uint_as_float(r[e]);
-        const int64_t c = (int64_t)qt * C::kBn + 96 * half + 32 * i;
+        const int64_t c = (int64_t)qt * 256 + cc;
         store_block(q, out + 2048 * (warp - 2), row - lane, c, v);
         if (q.flags & kFp4Sym) store_mirror(q, row, c, v);
       }
+      tc_fence_before();
     }
   }
   __syncwarp();
@@ -769,7 +760,7 @@ cudaError_t launch_bn(const Fp4GemmParams &p, int split, cudaStream_t s) {
 cudaError_t launch_fp4_gemm(const Fp4GemmParams &p, int bn, int split, bool nv, cudaStream_t s) {
   if (p.total_tiles <= 0) return cudaSuccess;
   switch (bn) {
-    case 192:
+    case kFp4PairBn:
       if (p.nprob <= kFewFp4Prob) return nv ? launch_pair<true, kFewFp4Prob>(p, s) : launch_pair<false, kFewFp4Prob>(p, s);
       return nv ? launch_pair<true, kMaxFp4Prob>(p, s) : launch_pair<false, kMaxFp4Prob>(p, s);
     case 16: return nv ? launch_bn<16, true>(p, split, s) : launch_bn<16, false>(p, split, s);

@@ -508,7 +508,7 @@ cudaError_t launch_fp4_dequantize(const Fp4Params &p, cudaStream_t s);
 // bn: Q rows of a tile: 16, 32, 64 or 128 (below 128 only with one tile along Q) on single CTAs with 128 rows of
 // P, `split` CTAs of a cluster sharing a tile's columns (1, 2, 4 or 8); or kFp4PairBn on CTA pairs with
 // 256 rows of P (split 1, kt > 0, kFp4DTrans unset).
-constexpr int kFp4PairBn = 192;
+constexpr int kFp4PairBn = 256;
 cudaError_t launch_fp4_gemm(const Fp4GemmParams &p, int bn, int split, bool nv, cudaStream_t s);
 // Tensor maps of a 4-bit matrix for the products: `rows` rows of codes a box; `steps` steps of 256 columns and
 // `row_tiles` row tiles of scales a box.
