@@ -231,49 +231,49 @@ __global__ void __launch_bounds__(kThreads, 2) fp4_gemm_kernel(const __grid_cons
   if (p.clear_status && blockIdx.x == 0 && threadIdx.x == 0) *p.status = 0;
 
   if (warp == 0) {
-    if (lane == 0) {
-      int stage = 0;
-      uint32_t phase = 0;
-      int last_parity[C::kStages];
+    int stage = 0;
+    uint32_t phase = 0;
+    int last_parity[C::kStages];
 #pragma unroll
-      for (int s = 0; s < C::kStages; ++s) last_parity[s] = -1;
-      for (int kb = k0; kb < k1; ++kb) {
-        if (!mbar_wait(empty(stage), phase ^ 1u, limit)) {
-          set_status(p.status, kTimeoutBit);
-          break;
-        }
-        const uint32_t sp = base + stage * C::kStage, sq = sp + C::kPBytes, ss = sq + C::kQBytes;
+    for (int s = 0; s < C::kStages; ++s) last_parity[s] = -1;
+    for (int kb = k0; kb < k1; ++kb) {
+      if (!mbar_wait_warp(empty(stage), phase ^ 1u, limit)) {
+        if (lane == 0) set_status(p.status, kTimeoutBit);
+        break;
+      }
+      const uint32_t sp = base + stage * C::kStage, sq = sp + C::kPBytes, ss = sq + C::kQBytes;
+      if (elect_one()) {
         mbar_arrive_expect_tx(full(stage), C::kStage);
-#pragma unroll
-        for (int s = 0; s < C::kStages; ++s)
-          if (s == stage) last_parity[s] = (int)phase;
         tma_load_2d(sp, &q.pc, kb * 128, pt * 128, full(stage));
         tma_load_2d(sq, &q.qc, kb * 128, qt * BN, full(stage));
         tma_load_3d(ss, &q.ps, 0, kb * C::kSTiles, pt, full(stage));
         tma_load_3d(ss + C::kPs, &q.qs, 0, kb * C::kSTiles, qt, full(stage));
-        if (++stage == C::kStages) {
-          stage = 0;
-          phase ^= 1u;
-        }
       }
-      // every load that was started must have landed before this CTA leaves
+      __syncwarp();
 #pragma unroll
       for (int s = 0; s < C::kStages; ++s)
-        if (last_parity[s] >= 0 && !mbar_wait(full(s), (uint32_t)last_parity[s], limit)) set_status(p.status, kTimeoutBit);
+        if (s == stage) last_parity[s] = (int)phase;
+      if (++stage == C::kStages) {
+        stage = 0;
+        phase ^= 1u;
+      }
     }
+    // every load that was started must have landed before this CTA leaves
+#pragma unroll
+    for (int s = 0; s < C::kStages; ++s)
+      if (last_parity[s] >= 0 && !mbar_wait_warp(full(s), (uint32_t)last_parity[s], limit) && lane == 0)
+        set_status(p.status, kTimeoutBit);
   } else if (warp == 1) {
-    if (lane == 0) {
-      int stage = 0;
-      uint32_t phase = 0;
-      bool ok = true;
-      for (int kb = k0; kb < k1; ++kb) {
-        if (!mbar_wait(full(stage), phase, limit)) {
-          set_status(p.status, kTimeoutBit);
-          ok = false;
-          break;
-        }
-        tc_fence_after();
-        const uint32_t sp = base + stage * C::kStage, sq = sp + C::kPBytes, ss = sq + C::kQBytes;
+    int stage = 0;
+    uint32_t phase = 0;
+    for (int kb = k0; kb < k1; ++kb) {
+      if (!mbar_wait_warp(full(stage), phase, limit)) {
+        if (lane == 0) set_status(p.status, kTimeoutBit);
+        break;
+      }
+      tc_fence_after();
+      const uint32_t sp = base + stage * C::kStage, sq = sp + C::kPBytes, ss = sq + C::kQBytes;
+      if (elect_one()) {
 #pragma unroll
         for (int j = 0; j < C::kSTiles; ++j) {
           tc_cp_scales(tmem + C::kPsCol + 4 * j, smem_desc_scales(ss + 512 * j));
@@ -288,12 +288,13 @@ __global__ void __launch_bounds__(kThreads, 2) fp4_gemm_kernel(const __grid_cons
                          kb != k0 || k != 0);
         }
         tc_commit(empty(stage));
-        if (++stage == C::kStages) {
-          stage = 0;
-          phase ^= 1u;
-        }
+        if (kb + 1 == k1) tc_commit(done);
       }
-      if (ok && k1 > k0) tc_commit(done);
+      __syncwarp();
+      if (++stage == C::kStages) {
+        stage = 0;
+        phase ^= 1u;
+      }
     }
   }
   // Warps 2-5: lanes 32 (warp mod 4) .. + 31 of the accumulator.  The rest waits for them below.
@@ -304,8 +305,8 @@ __global__ void __launch_bounds__(kThreads, 2) fp4_gemm_kernel(const __grid_cons
   const float g = q.pg ? *q.pg * *q.qg : 1.f;
   const bool trans = q.flags & kFp4DTrans, sym = q.flags & kFp4Sym;
   constexpr int N = BN < 32 ? BN : 32;
-  if (epi && have && !mbar_wait(done, 0, limit)) {
-    set_status(p.status, kTimeoutBit);
+  if (epi && have && !mbar_wait_warp(done, 0, limit)) {
+    if (lane == 0) set_status(p.status, kTimeoutBit);
     have = false;
   }
   __syncwarp();
@@ -394,17 +395,16 @@ __global__ void __launch_bounds__(kThreads, 2) fp4_gemm_kernel(const __grid_cons
 
 // 256 x 256 tiles on CTA pairs, persistent.  What bounds them is shared memory: a step of 256 columns writes 32 KB of
 // codes and 3 or 6 KB of scales into a CTA's and reads them for 513 clocks of MMAs (narrower tiles move more
-// bytes per MMA: 256 x 192 took 65 us where this takes 45, 8192 x 6144 x 2048 NVFP4).
+// bytes per MMA: 256 x 192 with the scales copied the same way was slower, 8192 x 6144 x 2048 NVFP4).
 //
 // Two accumulators of 256 columns and the scales do not fit the 512 columns of tensor memory, so the second
-// accumulator starts 192 (MX) or 160 columns after the first.  The epilogue drains the shared columns
+// accumulator starts 192 columns after the first.  The epilogue drains the 64 shared columns
 // first and hands them over; the next tile's MMAs run beside the rest of it.
 //
-// The scales are loaded beside the codes and copied into tensor memory by four warps of their own, whose
-// commits hand the buffers to the MMA warp: one thread starts a tcgen05.cp about every 70 clocks, and a
-// step needs 6 (MX) or 12 (NV) of them; copies of several warps run at the same time, and beside the
-// MMAs (83 us with the copies in the MMA warp).  A step's scales are 24 (MX) or 48 columns, a third for this
-// CTA's rows of P, the others for all rows of Q; two buffers.
+// The MMA warp copies a step's scales into tensor memory ahead of its MMAs: 24 (MX) or 48 columns, a third for this
+// CTA's rows of P, the others for all rows of Q.  Copies and MMAs of one thread run in order and
+// overlap.  The load and MMA warps stay converged and elect a lane to issue (see elect_one; with `lane == 0`
+// code the product above took 83 us, with four more warps for the copies 63 us).
 template <bool NV>
 struct PairCfg {
   static constexpr int kBn = kFp4PairBn;
@@ -416,14 +416,12 @@ struct PairCfg {
   static constexpr int kStages = 5;
   static constexpr int kOut = 8 * 2048;                      // a block of D for each epilogue warp
   static constexpr int kSmem = kStages * kStage + kOut + 1024 + 256;
-  static constexpr int kCols = 12 * kSTiles, kQCol = 4 * kSTiles, kBufs = 2;   // a step's scales: P's, Q's
-  static constexpr int kShared = NV ? 96 : 64, kShift = 256 - kShared;         // between the accumulators
-  static constexpr int kScales = kShift + 256;
-  static_assert(kStage % 1024 == 0 && kSmem <= 232448 && kScales + kCols * kBufs <= 512, "fits");
+  static constexpr int kShared = 64, kShift = 256 - kShared; // between the accumulators
+  static constexpr int kPsCol = kShift + 256, kQsCol = kPsCol + 4 * kSTiles;   // a step's scales
+  static_assert(kStage % 1024 == 0 && kSmem <= 232448 && kQsCol + 8 * kSTiles <= 512, "fits");
 };
-constexpr int kPairEpiWarps = 8, kPairCopyWarps = 4;
-constexpr int kLoadScalesWarp = 2 + kPairEpiWarps, kFirstCopyWarp = kLoadScalesWarp + 1;
-constexpr int kPairThreads = 32 * (kFirstCopyWarp + kPairCopyWarps);
+constexpr int kPairEpiWarps = 8;
+constexpr int kPairThreads = 64 + 32 * kPairEpiWarps;
 constexpr uint32_t kPeerMask = 0xFEFFFFFFu;                  // clears the CTA-rank bit of a cluster address
 
 template <bool NV, int NP>
@@ -433,15 +431,12 @@ __global__ void __launch_bounds__(kPairThreads, 1) fp4_pair_kernel(const __grid_
   uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t *out = smem + C::kStages * C::kStage;
   uint64_t *bars = reinterpret_cast<uint64_t *>(out + C::kOut);
-  constexpr int kBars = 2 * C::kStages + 2 * C::kBufs + 2;
+  constexpr int kBars = 2 * C::kStages + 2;
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + kBars);
   const uint32_t base = smem_u32(smem), bar_base = smem_u32(bars);
   auto full = [&](int s) { return bar_base + 8u * s; };                       // both CTAs' loads (leader's)
   auto empty = [&](int s) { return bar_base + 8u * (C::kStages + s); };
-  const uint32_t after = bar_base + 8u * (2 * C::kStages);
-  auto bfull = [&](int b) { return after + 8u * b; };                         // a buffer of scales (leader's)
-  auto bempty = [&](int b) { return after + 8u * (C::kBufs + b); };
-  const uint32_t tfull = after + 8u * (2 * C::kBufs), tfree = tfull + 8u;     // tfree: the leader's
+  const uint32_t tfull = bar_base + 8u * (2 * C::kStages), tfree = tfull + 8u;   // tfree: the leader's
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = cta_rank();
@@ -452,10 +447,6 @@ __global__ void __launch_bounds__(kPairThreads, 1) fp4_pair_kernel(const __grid_
     for (int s = 0; s < C::kStages; ++s) {
       mbar_init(full(s), 1);
       mbar_init(empty(s), 1);
-    }
-    for (int b = 0; b < C::kBufs; ++b) {
-      mbar_init(bfull(b), kPairCopyWarps);
-      mbar_init(bempty(b), 1);
     }
     mbar_init(tfull, 1);
     mbar_init(tfree, 2 * kPairEpiWarps);   // one arrival per epilogue warp of both CTAs
@@ -480,152 +471,93 @@ __global__ void __launch_bounds__(kPairThreads, 1) fp4_pair_kernel(const __grid_
   if (p.clear_status && blockIdx.x == 0 && threadIdx.x == 0) *p.status = 0;
 
   if (warp == 0) {
-    if (lane == 0) {
-      // ------------------------------------------------------------ codes (both CTAs)
-      int stage = 0;
-      uint32_t phase = 0;
-      int last_parity[C::kStages];
+    // -------------------------------------------------------------- loads (both CTAs)
+    int stage = 0;
+    uint32_t phase = 0;
+    int last_parity[C::kStages];
 #pragma unroll
-      for (int s = 0; s < C::kStages; ++s) last_parity[s] = -1;
-      bool ok = true;
-      for (int tile = cid; ok && tile < p.total_tiles; tile += ncl) {
-        const Fp4Prob &q = p.prob[find_prob(p, tile)];
-        int pt, qt;
-        tile_of<256, 256>(q, tile - q.tile_begin, pt, qt);
-        const int prow = pt * 256 + 128 * (int)rank, qrow = qt * 256 + 128 * (int)rank;
-        for (int kb = 0; kb < q.kt; ++kb) {
-          if (!mbar_wait(empty(stage), phase ^ 1u, limit)) {
-            set_status(p.status, kTimeoutBit);
-            ok = false;
-            break;
-          }
-          const uint32_t sp = base + stage * C::kStage, sq = sp + C::kHalf;
-          const uint32_t fb = full(stage) & kPeerMask;      // the leader's barrier
-          if (leader) {
-            mbar_arrive_expect_tx(full(stage), 2 * C::kStage);
-#pragma unroll
-            for (int s = 0; s < C::kStages; ++s)
-              if (s == stage) last_parity[s] = (int)phase;
-          }
+    for (int s = 0; s < C::kStages; ++s) last_parity[s] = -1;
+    bool ok = true;
+    for (int tile = cid; ok && tile < p.total_tiles; tile += ncl) {
+      const Fp4Prob &q = p.prob[find_prob(p, tile)];
+      int pt, qt;
+      tile_of<256, 256>(q, tile - q.tile_begin, pt, qt);
+      const int prow = pt * 256 + 128 * (int)rank, qrow = qt * 256 + 128 * (int)rank;
+      for (int kb = 0; kb < q.kt; ++kb) {
+        ok = mbar_wait_warp(empty(stage), phase ^ 1u, limit);
+        if (!ok) break;
+        const uint32_t sp = base + stage * C::kStage, sq = sp + C::kHalf, ss = sq + C::kHalf;
+        const uint32_t fb = full(stage) & kPeerMask;      // the leader's barrier
+        if (elect_one()) {
+          if (leader) mbar_arrive_expect_tx(full(stage), 2 * C::kStage);
           tma_load_2sm(sp, &q.pc, kb * 128, prow, fb);
           tma_load_2sm(sq, &q.qc, kb * 128, qrow, fb);
-          if (++stage == C::kStages) {
-            stage = 0;
-            phase ^= 1u;
-          }
+          tma_load_3d_2sm(ss, &q.ps, 0, kb * C::kSTiles, pt * 2 + (int)rank, fb);
+          tma_load_3d_2sm(ss + C::kRt, &q.qs, 0, kb * C::kSTiles, qt * 2, fb);
         }
-      }
-      if (leader) {
-        // every load of the pair that was armed must have landed
+        __syncwarp();
 #pragma unroll
         for (int s = 0; s < C::kStages; ++s)
-          if (last_parity[s] >= 0 && !mbar_wait(full(s), (uint32_t)last_parity[s], limit)) set_status(p.status, kTimeoutBit);
+          if (s == stage) last_parity[s] = (int)phase;
+        if (++stage == C::kStages) {
+          stage = 0;
+          phase ^= 1u;
+        }
       }
     }
+    if (!ok && lane == 0) set_status(p.status, kTimeoutBit);
+    if (leader) {
+      // every load of the pair that was armed must have landed
+#pragma unroll
+      for (int s = 0; s < C::kStages; ++s)
+        if (last_parity[s] >= 0 && !mbar_wait_warp(full(s), (uint32_t)last_parity[s], limit) && lane == 0)
+          set_status(p.status, kTimeoutBit);
+    }
   } else if (warp == 1) {
-    if (lane == 0 && leader) {
-      // ------------------------------------------------------------ MMAs (leader)
-      int stage = 0, tl = 0, buf = 0;
-      uint32_t phase = 0, bphase = 0;
+    if (leader) {
+      // ------------------------------------------------------------ copies and MMAs (leader)
+      int stage = 0, tl = 0;
+      uint32_t phase = 0;
       bool ok = true;
       for (int tile = cid; ok && tile < p.total_tiles; tile += ncl, ++tl) {
         const int kt = p.prob[find_prob(p, tile)].kt;
         // the columns that this tile shares with the one before have been drained, and with them all
         // of the tile before that
-        ok = tl == 0 || mbar_wait(tfree, (uint32_t)(tl - 1) & 1u, limit);
+        ok = tl == 0 || mbar_wait_warp(tfree, (uint32_t)(tl - 1) & 1u, limit);
         if (!ok) break;
         tc_fence_after();
         const uint32_t d = tmem + (uint32_t)((tl & 1) * C::kShift);
-        for (int kb = 0; ok && kb < kt; ++kb) {
-          ok = mbar_wait(full(stage), phase, limit);
-          if (!ok) break;
-          const uint32_t sp = base + stage * C::kStage, sq = sp + C::kHalf;
-          ok = mbar_wait(bfull(buf), bphase, limit);
+        for (int kb = 0; kb < kt; ++kb) {
+          ok = mbar_wait_warp(full(stage), phase, limit);
           if (!ok) break;
           tc_fence_after();
-          const uint32_t sc = tmem + C::kScales + C::kCols * buf;
+          const uint32_t sp = base + stage * C::kStage, sq = sp + C::kHalf, ss = sq + C::kHalf;
+          if (elect_one()) {
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            // 64 columns: 32 bytes inside the swizzled rows; MX: half of a scale word, NV: a whole one
-            const int j = NV ? k : k >> 1, id = NV ? 0 : 2 * (k & 1);
-            tc_mma2_fp4<NV>(d, smem_desc_sw128(sp + 32 * k, 16, 1024), smem_desc_sw128(sq + 32 * k, 16, 1024),
-                            idesc_fp4(256, C::kBn, NV, id), sc + 4 * j, sc + C::kQCol + 8 * j, (kb | k) != 0);
-          }
-          tc_commit2_mc(bempty(buf), 0x1);
-          tc_commit2_mc(empty(stage), 0x3);
-          if (++buf == C::kBufs) {
-            buf = 0;
-            bphase ^= 1u;
-          }
-          if (++stage == C::kStages) {
-            stage = 0;
-            phase ^= 1u;
-          }
-        }
-        if (ok) tc_commit2_mc(tfull, 0x3);
-      }
-      if (!ok) set_status(p.status, kTimeoutBit);
-    }
-  } else if (warp == kLoadScalesWarp) {
-    if (lane == 0) {
-      // ------------------------------------------------------------ scales (both CTAs)
-      int stage = 0;
-      uint32_t phase = 0;
-      bool ok = true;
-      for (int tile = cid; ok && tile < p.total_tiles; tile += ncl) {
-        const Fp4Prob &q = p.prob[find_prob(p, tile)];
-        int pt, qt;
-        tile_of<256, 256>(q, tile - q.tile_begin, pt, qt);
-        for (int kb = 0; kb < q.kt; ++kb) {
-          ok = mbar_wait(empty(stage), phase ^ 1u, limit);
-          if (!ok) break;               // the warp that loads the codes reports it
-          const uint32_t ss = base + stage * C::kStage + C::kCodes;
-          const uint32_t fb = full(stage) & kPeerMask;
-          tma_load_3d_2sm(ss, &q.ps, 0, kb * C::kSTiles, pt * 2 + (int)rank, fb);
-          tma_load_3d_2sm(ss + C::kRt, &q.qs, 0, kb * C::kSTiles, qt * 2, fb);
-          if (++stage == C::kStages) {
-            stage = 0;
-            phase ^= 1u;
-          }
-        }
-      }
-    }
-  } else if (warp >= kFirstCopyWarp) {
-    if (lane == 0 && leader) {
-      // ------------------------------------------------------------ scales to tensor memory (leader)
-      const int w = warp - kFirstCopyWarp;
-      int stage = 0, buf = 0;
-      uint32_t phase = 0, bphase = 0;
-      bool ok = true;
-      for (int tile = cid; ok && tile < p.total_tiles; tile += ncl) {
-        const int kt = p.prob[find_prob(p, tile)].kt;
-        for (int kb = 0; ok && kb < kt; ++kb) {
-          ok = mbar_wait(full(stage), phase, limit);
-          if (!ok) break;
-          const uint32_t ss = base + stage * C::kStage + C::kCodes;
-          ok = mbar_wait(bempty(buf), bphase ^ 1u, limit);
-          if (!ok) break;
-          tc_fence_after();
-          const uint32_t to = tmem + C::kScales + C::kCols * buf;
-          // tile j of row tile i: P's own rows (i = 0), Q's two
+            for (int j = 0; j < C::kSTiles; ++j) {
+              tc_cp2_scales(tmem + C::kPsCol + 4 * j, smem_desc_scales(ss + 512 * j));
 #pragma unroll
-          for (int c = 0; c < 3 * C::kSTiles; ++c) {
-            const int j = c % C::kSTiles, i = c / C::kSTiles;
-            if (c % kPairCopyWarps == w)
-              tc_cp2_scales(to + (i == 0 ? 4 * j : C::kQCol + 8 * j + 4 * (i - 1)), smem_desc_scales(ss + i * C::kRt + 512 * j));
+              for (int i = 0; i < 2; ++i)
+                tc_cp2_scales(tmem + C::kQsCol + 8 * j + 4 * i, smem_desc_scales(ss + (1 + i) * C::kRt + 512 * j));
+            }
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              // 64 columns: 32 bytes inside the swizzled rows; MX: half of a scale word, NV: a whole one
+              const int j = NV ? k : k >> 1, id = NV ? 0 : 2 * (k & 1);
+              tc_mma2_fp4<NV>(d, smem_desc_sw128(sp + 32 * k, 16, 1024), smem_desc_sw128(sq + 32 * k, 16, 1024),
+                              idesc_fp4(256, C::kBn, NV, id), tmem + C::kPsCol + 4 * j, tmem + C::kQsCol + 8 * j, (kb | k) != 0);
+            }
+            tc_commit2_mc(empty(stage), 0x3);
+            if (kb + 1 == kt) tc_commit2_mc(tfull, 0x3);
           }
-          tc_commit2_mc(bfull(buf), 0x1);
-          if (++buf == C::kBufs) {
-            buf = 0;
-            bphase ^= 1u;
-          }
+          __syncwarp();
           if (++stage == C::kStages) {
             stage = 0;
             phase ^= 1u;
           }
         }
       }
-      if (!ok) set_status(p.status, kTimeoutBit);
+      if (!ok && lane == 0) set_status(p.status, kTimeoutBit);
     }
   } else {
     // -------------------------------------------------------------- epilogue (both CTAs)
@@ -638,12 +570,8 @@ __global__ void __launch_bounds__(kPairThreads, 1) fp4_pair_kernel(const __grid_
       const float g = q.pg ? *q.pg * *q.qg : 1.f;
       const int64_t row = (int64_t)pt * 256 + 128 * rank + quarter * 32 + lane;
       const uint32_t acc = tmem + (uint32_t)((tl & 1) * C::kShift) + ((uint32_t)(quarter * 32) << 16);
-      // 32 columns at a time, the shared ones first: of three such chunks half 0 takes two, of two
-      // each half one
-      constexpr int kChunks = C::kShared / 32;
-      const int shared_c = (tl & 1) ? 0 : C::kShift, rest_c = (tl & 1) ? C::kShared : 0;
-      const int n_shared = kChunks - kChunks / 2 - (half ? kChunks & 1 : 0);
-      const int first_shared = half ? kChunks - kChunks / 2 : 0, first_rest = half ? 4 - (kChunks - kChunks / 2) : 0;
+      // 32 columns at a time: one of the two shared chunks first, then three others
+      const int shared_c = ((tl & 1) ? 0 : C::kShift) + 32 * half, rest_c = ((tl & 1) ? C::kShared : 0) + 96 * half;
       if (!mbar_wait_warp(tfull, (uint32_t)tl & 1u, limit)) {
         set_status(p.status, kTimeoutBit);
         break;
@@ -651,11 +579,11 @@ __global__ void __launch_bounds__(kPairThreads, 1) fp4_pair_kernel(const __grid_
       tc_fence_after();
 #pragma unroll 1
       for (int i = 0; i < 4; ++i) {
-        const int cc = i < n_shared ? shared_c + 32 * (first_shared + i) : rest_c + 32 * (first_rest + i - n_shared);
+        const int cc = i == 0 ? shared_c : rest_c + 32 * (i - 1);
         uint32_t r[32];
         tmem_ld32(acc + cc, r);
         tmem_ld_wait();
-        if (i == n_shared - 1) {
+        if (i == 0) {
           tc_fence_before();
           __syncwarp();
           if (lane == 0) remote_arrive_relaxed(mapa(tfree, 0));

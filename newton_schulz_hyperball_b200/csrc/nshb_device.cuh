@@ -139,13 +139,18 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, long lo
   return true;
 }
 
-// The same for a whole warp, with one lane at the barrier: 32 polling lanes of several warps hold up
-// the thread that issues the loads they wait for.
+// The same for a whole warp, which stays converged: every lane gets the same answer.
 __device__ __forceinline__ bool mbar_wait_warp(uint32_t bar, uint32_t parity, long long limit) {
-  bool ok = true;
-  if ((threadIdx.x & 31) == 0) ok = mbar_wait(bar, parity, limit);
-  __syncwarp();
-  return __shfl_sync(0xffffffffu, (int)ok, 0) != 0;
+  return __all_sync(0xffffffffu, mbar_wait(bar, parity, limit));
+}
+// True in one lane of a converged warp.  Code that issues tensor-core or copy instructions from a whole warp
+// under this predicate keeps their descriptors in uniform registers; under `lane == 0` each operand is moved
+// there first, about 70 clocks an instruction (measured: 12 tcgen05.cp and 4 MMAs of 128 clocks each take 798
+// clocks that way and 513 this way).
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+  return p != 0;
 }
 
 // ----------------------------------------------------- bulk async copy (no tensor map)
@@ -322,8 +327,7 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap *map
 __device__ __forceinline__ uint64_t smem_desc_scales(uint32_t saddr) {
   return (uint64_t)((saddr >> 4) & 0x3FFFu) | ((uint64_t)(128 >> 4) << 32) | ((uint64_t)1 << 46);
 }
-// Copies such a tile into four TMEM columns, once for each group of 32 lanes.  A thread can start one about every 70
-// clocks, whatever its form; copies of several warps run at the same time.
+// Copies such a tile into four TMEM columns, once for each group of 32 lanes.
 __device__ __forceinline__ void tc_cp_scales(uint32_t taddr, uint64_t desc) {
   asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc) : "memory");
 }
