@@ -87,7 +87,15 @@ Shape shape_of(int64_t m, int64_t n, int64_t kt, bool sym, bool pairs) {
     s.bn = q <= 16 ? 16 : q <= 32 ? 32 : 64;
   }
   s.tiles = count_tiles(p, q, 128, s.bn, sym);
-  while (s.split < 8 && s.split * 2 <= kt && s.tiles * s.split * 2 <= 2 * device_sms()) s.split *= 2;
+  // A step of 256 columns takes a lone CTA 0.3 us, joining the parts of a cluster 2 us (narrow tiles) to 4 us
+  // (128 x 128): split long sums of few tiles.  Measured: 1 x 2048 x 6144 in 8.5 us with 1 CTA a tile, 5.0 with
+  // 4, 4.5 with 8; 128 x 2048 x 8192 in 13.3, 8.7 and 9.9 us; but 1 x 6144 x 2048 in 4.1 and 4.8 us,
+  // 1024^3 in 5.2 and 9.1 us with 1 and 4.
+  const int64_t sms = device_sms();
+  const bool wide_tile = s.bn == 128;
+  if (kt >= (wide_tile ? 32 : 24) && s.tiles * 8 <= (wide_tile ? sms / 2 : sms)) s.split = 8;
+  else if (kt >= 16 && s.tiles * 4 <= sms) s.split = 4;
+  else if (kt >= (wide_tile ? 32 : 16) && s.tiles * 2 <= sms) s.split = 2;
   return s;
 }
 

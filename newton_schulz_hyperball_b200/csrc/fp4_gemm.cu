@@ -46,7 +46,7 @@ struct Cfg {
   static constexpr int kUsed = kQsCol + 4 * kSTiles;
   static constexpr int kTmem = kUsed <= 64 ? 64 : kUsed <= 128 ? 128 : 256;
   static_assert(kStage % 1024 == 0, "every stage starts on a swizzle atom");
-  static_assert(128 * BN * 4 <= kStages * kStage, "the partial sums fit the ring");
+  static_assert((128 + 64) * (BN + 4) * 4 <= kStages * kStage, "the partial sums and half a tile fit the ring");
 };
 
 template <class P>
@@ -170,13 +170,17 @@ __device__ __forceinline__ void store_block(const Fp4Prob &q, uint8_t *stage, in
 
 // The mirror image of such a block's elements below the diagonal.
 __device__ __forceinline__ void store_mirror(const Fp4Prob &q, int64_t row, int64_t c, const float (&v)[32]) {
-  if (row >= q.np) return;
+  const int64_t row0 = row - (threadIdx.x & 31);
+  if (c >= row0 + 31 || row >= q.np) return;
+  const bool f32 = q.flags & kFp4DF32, below = c + 31 < row0;   // else the block crosses the diagonal
 #pragma unroll
   for (int e = 0; e < 32; ++e) {
-    if (c + e >= row || c + e >= q.nq) break;
+    if (c + e >= q.nq) break;
     const int64_t at = (c + e) * q.ld + row;
-    if (q.flags & kFp4DF32) static_cast<float *>(q.d)[at] = v[e];
-    else static_cast<__nv_bfloat16 *>(q.d)[at] = __float2bfloat16_rn(v[e]);
+    if (below || c + e < row) {
+      if (f32) static_cast<float *>(q.d)[at] = v[e];
+      else static_cast<__nv_bfloat16 *>(q.d)[at] = __float2bfloat16_rn(v[e]);
+    }
   }
 }
 
@@ -346,20 +350,32 @@ __global__ void __launch_bounds__(kThreads, 2) fp4_gemm_kernel(const __grid_cons
       }
     }
   } else {
-    // The parts: column by column into this CTA's ring, which its own MMAs have left, then every CTA
-    // sums the columns that fall to it, part 0 first.
+    // The parts go into this CTA's ring, which its own MMAs have left: rows of kPitch floats, or column by
+    // column where D takes the transpose.  Then every CTA sums the rows (columns) that fall to it, part
+    // 0 first.
+    constexpr int kPitch = BN + 4;
     float *mine = reinterpret_cast<float *>(smem);
     if (epi) {
 #pragma unroll 1
       for (int c = 0; c < BN; c += N) {
         float v[N];
         if (have) read(c, v);
+        else {
 #pragma unroll
-        for (int e = 0; e < N; ++e) mine[(c + e) * 128 + row] = have ? v[e] : 0.f;
+          for (int e = 0; e < N; ++e) v[e] = 0.f;
+        }
+        if (trans) {
+#pragma unroll
+          for (int e = 0; e < N; ++e) mine[(c + e) * 128 + row] = v[e];
+        } else {
+#pragma unroll
+          for (int e = 0; e < N; e += 4)
+            *reinterpret_cast<float4 *>(mine + row * kPitch + c + e) = make_float4(v[e], v[e + 1], v[e + 2], v[e + 3]);
+        }
       }
     }
     cluster_sync();
-    if (epi) {
+    if (epi && trans) {
       // BN and parts are powers of two: a CTA takes 2 columns or more
       auto join = [&](int c, auto width) {
         constexpr int W = decltype(width)::value;
@@ -373,14 +389,57 @@ __global__ void __launch_bounds__(kThreads, 2) fp4_gemm_kernel(const __grid_cons
         }
 #pragma unroll
         for (int e = 0; e < W; ++e) v[e] *= g;
-        store_row<W>(q, (int64_t)pt * 128 + row, (int64_t)qt * BN + c, v, trans);
-        if (sym && pt != qt) store_row<W>(q, (int64_t)pt * 128 + row, (int64_t)qt * BN + c, v, true);
+        store_row<W>(q, (int64_t)pt * 128 + row, (int64_t)qt * BN + c, v, true);
       };
       const int each = BN / parts, c0 = each * part;
       if (each >= 8) {
         for (int c = c0; c < c0 + each; c += 8) join(c, std::integral_constant<int, 8>());
       } else {
         for (int c = c0; c < c0 + each; c += 2) join(c, std::integral_constant<int, 2>());
+      }
+    } else if (epi) {
+      constexpr int L = BN / 4, kRows = 32 / L;           // lanes of a row, rows of an instruction
+      const int w = warp - 2, n = 128 / parts, r0 = n * part;
+      float *sum = mine + 128 * kPitch;                   // n rows, behind the parts
+#pragma unroll 4
+      for (int i = w * kRows; i < n; i += 4 * kRows) {
+        const int r = i + lane / L, c = 4 * (lane % L);
+        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int k = 0; k < parts; ++k) {
+          const float4 x = ld_cluster4(mapa(base + (uint32_t)(((r0 + r) * kPitch + c) * 4), (uint32_t)k));
+          v.x += x.x; v.y += x.y; v.z += x.z; v.w += x.w;
+        }
+        *reinterpret_cast<float4 *>(sum + r * kPitch + c) = make_float4(g * v.x, g * v.y, g * v.z, g * v.w);
+      }
+      named_barrier(1, 128);
+      const int64_t p0 = (int64_t)pt * 128 + r0, q0 = (int64_t)qt * BN;
+      const int rows = (int)(q.np - p0 < n ? q.np - p0 : n), cols = (int)(q.nq - q0 < BN ? q.nq - q0 : BN);
+      const bool f32 = q.flags & kFp4DF32;
+      if ((q.flags & kFp4DVec) && cols == BN) {
+        for (int i = w * kRows; i < rows; i += 4 * kRows) {
+          const int r = i + lane / L, c = 4 * (lane % L);
+          const float4 x = *reinterpret_cast<const float4 *>(sum + r * kPitch + c);
+          const int64_t at = (p0 + r) * q.ld + q0 + c;
+          if (r >= rows) continue;
+          if (f32) *reinterpret_cast<float4 *>(static_cast<float *>(q.d) + at) = x;
+          else *reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(q.d) + at) = make_uint2(pack_bf16(x.x, x.y), pack_bf16(x.z, x.w));
+        }
+      } else {
+        for (int r = w; r < rows; r += 4)
+          for (int c = lane; c < cols; c += 32) {
+            const int64_t at = (p0 + r) * q.ld + q0 + c;
+            if (f32) static_cast<float *>(q.d)[at] = sum[r * kPitch + c];
+            else static_cast<__nv_bfloat16 *>(q.d)[at] = __float2bfloat16_rn(sum[r * kPitch + c]);
+          }
+      }
+      if (sym && pt != qt) {
+        // the mirror image: rows run along D's columns
+        for (int c = w; c < cols; c += 4)
+          for (int r = lane; r < rows; r += 32) {
+            const int64_t at = (q0 + c) * q.ld + p0 + r;
+            if (f32) static_cast<float *>(q.d)[at] = sum[r * kPitch + c];
+            else static_cast<__nv_bfloat16 *>(q.d)[at] = __float2bfloat16_rn(sum[r * kPitch + c]);
+          }
       }
     }
     cluster_sync();   // no CTA leaves while another may still read its shared memory

@@ -75,7 +75,8 @@ def product(ops_a, ops_b, dtype, lds=None):
 
 SIZES = [(1, 1, 1), (1, 128, 64), (128, 128, 64), (128, 128, 128), (128, 128, 256), (128, 128, 1024), (1, 16, 31),
          (3, 5, 17), (1, 300, 2048), (16, 257, 300), (17, 129, 512), (33, 1000, 640), (64, 640, 2049), (65, 66, 67),
-         (300, 1, 700), (300, 40, 130), (129, 255, 257), (256, 384, 511), (1000, 777, 1333), (130, 2000, 96)]
+         (300, 1, 700), (300, 40, 130), (1, 2000, 4096), (2, 130, 6200), (20, 500, 5000), (64, 256, 8192), (130, 140, 8192),
+         (200, 300, 4100), (1100, 500, 8192), (257, 7, 6145), (129, 255, 257), (256, 384, 511), (1000, 777, 1333), (130, 2000, 96)]
 
 
 @pytest.mark.parametrize("fmt", [MX, NV])
@@ -90,7 +91,8 @@ def test_products(fmt, dtype, size):
 
 
 @pytest.mark.parametrize("fmt", [MX, NV])
-@pytest.mark.parametrize("size", [(1, 1), (40, 100), (128, 300), (129, 64), (400, 1000), (768, 2000)])
+@pytest.mark.parametrize("size", [(1, 1), (40, 100), (128, 300), (129, 64), (400, 1000), (768, 2000), (300, 8200),
+                                  (500, 4097)])
 def test_gram(fmt, size):
     d, k = size
     a, av = operand(d, k, fmt, 3)
