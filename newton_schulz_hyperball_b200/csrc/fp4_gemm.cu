@@ -15,8 +15,8 @@
 // Enough 256 x 256 tiles to fill the GPU go to CTA pairs (fp4_pair_kernel): a pair reads 64 bytes of
 // codes per clock and SM for the work that single CTAs with 128 x 128 tiles need 128 for.
 //
-// Roles of the single CTA (192 threads): warp 0 issues the loads of the ring, warp 1 the copies and MMAs, warps
-// 2-5 drain the accumulator.  Every wait is bounded.
+// Roles of the single CTA (320 threads): warp 0 issues the loads of the ring, warp 1 the copies and MMAs, warps
+// 2-9 drain the accumulator.  Every wait is bounded.
 #include <cuda.h>
 #include <cuda_runtime.h>
 #include <cuda_bf16.h>
@@ -29,7 +29,8 @@
 namespace nshb {
 namespace {
 
-constexpr int kThreads = 192;
+constexpr int kEpiWarps = 8;
+constexpr int kThreads = 64 + 32 * kEpiWarps;
 constexpr uint32_t kTimeoutBit = 0x4u;
 
 template <int BN, bool NV>
@@ -153,13 +154,15 @@ __device__ __forceinline__ void store_block(const Fp4Prob &q, uint8_t *stage, in
       }
     } else if (f32) {
       // two rows at a time
-      for (int r = lane >> 4; r < rows; r += 2) {
-        const int e = lane & 15;
-        if (e < have)
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        const int r = 2 * i + (lane >> 4), e = lane & 15;
+        if (r < rows && e < have)
           *reinterpret_cast<uint32_t *>(dp + r * pitch + 4 * e) =
               *reinterpret_cast<const uint32_t *>(stage + r * 64 + (((e >> 2) ^ ((r >> 1) & 3)) << 4) + 4 * (e & 3));
       }
     } else {
+#pragma unroll 8
       for (int r = 0; r < rows; ++r)
         if (lane < have)
           *reinterpret_cast<unsigned short *>(dp + r * pitch + 2 * lane) =
@@ -301,8 +304,11 @@ __global__ void __launch_bounds__(kThreads, 2) fp4_gemm_kernel(const __grid_cons
       }
     }
   }
-  // Warps 2-5: lanes 32 (warp mod 4) .. + 31 of the accumulator.  The rest waits for them below.
-  const int quarter = warp & 3;
+  // Warps 2-9: lanes 32 (warp mod 4) .. + 31 of the accumulator, each half of its columns (of narrow tiles
+  // warps 2-5 all of them).  The rest waits for them below.
+  const int quarter = warp & 3, half = (warp - 2) >> 2;
+  constexpr int kHalfBn = BN >= 64 ? BN / 2 : BN;
+  const int c_begin = half * kHalfBn, c_end = c_begin + kHalfBn < BN ? c_begin + kHalfBn : BN;
   const int row = quarter * 32 + lane;
   const bool epi = warp >= 2;
   bool have = k1 > k0;
@@ -329,7 +335,7 @@ __global__ void __launch_bounds__(kThreads, 2) fp4_gemm_kernel(const __grid_cons
     const int64_t at = (int64_t)qt * BN + c;
     if constexpr (N == 32) {
       // the ring is free: this CTA's MMAs are done
-      if (!trans) store_block(q, smem + 2048 * quarter, (int64_t)pt * 128 + 32 * quarter, at, v);
+      if (!trans) store_block(q, smem + 2048 * (warp - 2), (int64_t)pt * 128 + 32 * quarter, at, v);
       else store_row<N>(q, (int64_t)pt * 128 + row, at, v, true);
     } else {
       store_row<N>(q, (int64_t)pt * 128 + row, at, v, trans);
@@ -339,7 +345,7 @@ __global__ void __launch_bounds__(kThreads, 2) fp4_gemm_kernel(const __grid_cons
   if (!SPLIT) {
     if (epi) {
 #pragma unroll 1
-      for (int c = 0; c < BN; c += N) {
+      for (int c = c_begin; c < c_end; c += N) {
         float v[N];
         if (have) read(c, v);
         else {
@@ -357,7 +363,7 @@ __global__ void __launch_bounds__(kThreads, 2) fp4_gemm_kernel(const __grid_cons
     float *mine = reinterpret_cast<float *>(smem);
     if (epi) {
 #pragma unroll 1
-      for (int c = 0; c < BN; c += N) {
+      for (int c = c_begin; c < c_end; c += N) {
         float v[N];
         if (have) read(c, v);
         else {
@@ -392,17 +398,17 @@ __global__ void __launch_bounds__(kThreads, 2) fp4_gemm_kernel(const __grid_cons
         store_row<W>(q, (int64_t)pt * 128 + row, (int64_t)qt * BN + c, v, true);
       };
       const int each = BN / parts, c0 = each * part;
-      if (each >= 8) {
-        for (int c = c0; c < c0 + each; c += 8) join(c, std::integral_constant<int, 8>());
+      if (each >= 16) {
+        for (int c = c0 + 8 * half; c < c0 + each; c += 16) join(c, std::integral_constant<int, 8>());
       } else {
-        for (int c = c0; c < c0 + each; c += 2) join(c, std::integral_constant<int, 2>());
+        for (int c = c0 + 2 * half; c < c0 + each; c += 4) join(c, std::integral_constant<int, 2>());
       }
     } else if (epi) {
       constexpr int L = BN / 4, kRows = 32 / L;           // lanes of a row, rows of an instruction
       const int w = warp - 2, n = 128 / parts, r0 = n * part;
       float *sum = mine + 128 * kPitch;                   // n rows, behind the parts
 #pragma unroll 4
-      for (int i = w * kRows; i < n; i += 4 * kRows) {
+      for (int i = w * kRows; i < n; i += kEpiWarps * kRows) {
         const int r = i + lane / L, c = 4 * (lane % L);
         float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
         for (int k = 0; k < parts; ++k) {
@@ -411,12 +417,12 @@ __global__ void __launch_bounds__(kThreads, 2) fp4_gemm_kernel(const __grid_cons
         }
         *reinterpret_cast<float4 *>(sum + r * kPitch + c) = make_float4(g * v.x, g * v.y, g * v.z, g * v.w);
       }
-      named_barrier(1, 128);
+      named_barrier(1, 32 * kEpiWarps);
       const int64_t p0 = (int64_t)pt * 128 + r0, q0 = (int64_t)qt * BN;
       const int rows = (int)(q.np - p0 < n ? q.np - p0 : n), cols = (int)(q.nq - q0 < BN ? q.nq - q0 : BN);
       const bool f32 = q.flags & kFp4DF32;
       if ((q.flags & kFp4DVec) && cols == BN) {
-        for (int i = w * kRows; i < rows; i += 4 * kRows) {
+        for (int i = w * kRows; i < rows; i += kEpiWarps * kRows) {
           const int r = i + lane / L, c = 4 * (lane % L);
           const float4 x = *reinterpret_cast<const float4 *>(sum + r * kPitch + c);
           const int64_t at = (p0 + r) * q.ld + q0 + c;
@@ -425,7 +431,7 @@ __global__ void __launch_bounds__(kThreads, 2) fp4_gemm_kernel(const __grid_cons
           else *reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(q.d) + at) = make_uint2(pack_bf16(x.x, x.y), pack_bf16(x.z, x.w));
         }
       } else {
-        for (int r = w; r < rows; r += 4)
+        for (int r = w; r < rows; r += kEpiWarps)
           for (int c = lane; c < cols; c += 32) {
             const int64_t at = (p0 + r) * q.ld + q0 + c;
             if (f32) static_cast<float *>(q.d)[at] = sum[r * kPitch + c];
@@ -434,7 +440,7 @@ __global__ void __launch_bounds__(kThreads, 2) fp4_gemm_kernel(const __grid_cons
       }
       if (sym && pt != qt) {
         // the mirror image: rows run along D's columns
-        for (int c = w; c < cols; c += 4)
+        for (int c = w; c < cols; c += kEpiWarps)
           for (int r = lane; r < rows; r += 32) {
             const int64_t at = (q0 + c) * q.ld + p0 + r;
             if (f32) static_cast<float *>(q.d)[at] = sum[r * kPitch + c];
