@@ -5,11 +5,15 @@
 //
 // Bound by HBM: 2 (or 4) bytes read and 0.53 (0.56) written per element.  A CTA takes a tile of 128 rows x 128
 // columns, so that every 128-byte line of the source, every 64-byte piece of a row of codes and
-// every 512-byte tile of scales is moved whole; a thread quantises 32 columns of a row at a time.  For the
-// transpose the tile goes through shared memory as 32-bit words, whose place is permuted by
+// every 512-byte tile of scales is moved whole.  A lane takes 8 columns, 16 lanes a row: each load and store
+// instruction of a warp covers two whole pieces of rows (32 columns a lane, 64 bytes apart, took
+// twice as long for the values).  The CTAs are persistent and load ahead: a batch of rows of the same or the next
+// tile is under way while one is processed.  For the transpose the tile goes through shared memory as 32-bit words, whose place is permuted by
 // the 32-row group (word ^ 8 group), so that the four groups of eight columns that a warp reads
 // fall into different banks.
 #include <cuda_runtime.h>
+
+#include <type_traits>
 
 #include "nshb_device.cuh"
 #include "nshb_internal.h"
@@ -112,55 +116,78 @@ struct Cols32 {
   }
 };
 
+// 8 consecutive columns as they were loaded.
+template <bool F32>
+struct Cols8 {
+  static constexpr int NW = F32 ? 8 : 4;
+  uint32_t w[NW];
+  __device__ __forceinline__ float get(int e) const {
+    if (F32) return __uint_as_float(w[F32 ? e : 0]);
+    return (e & 1) ? bf16hi(w[e >> 1]) : bf16lo(w[e >> 1]);
+  }
+  __device__ __forceinline__ uint32_t top() const {
+    uint32_t m = 0;
+    if constexpr (F32) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) m = max(m, w[e] & 0x7fffffffu);
+      return m;
+    } else {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) m = __vmaxu2(m, w[e] & 0x7fff7fffu);
+      return max(m << 16, m & 0xffff0000u);
+    }
+  }
+};
+
+// The scale byte of a block whose largest magnitude has the bits `top`, and what its elements are
+// multiplied with (MX) or divided by (NV: s, and its reciprocal) to become codes.
+template <bool NV>
+__device__ __forceinline__ uint32_t block_scale(uint32_t top, float down, float &s, float &r) {
+  const bool bad = top >= 0x7f800000u;
+  if (!NV) {
+    const uint32_t be = top >> 23;
+    const uint32_t b = be > 2 ? be - 2 : 0;              // biased exponent of the scale, 2^-127 at least
+    r = __uint_as_float((254u - b) << 23);               // exact: a power of two
+    return bad ? 255u : b;
+  }
+  const float m = (bad ? 0.f : __uint_as_float(top)) * down;
+  const float q6 = __fdiv_rn(m, 6.f);
+  const uint32_t sb = to_e4m3(odd(q6, fmaf(-q6, 6.f, m), m));
+  s = from_e4m3(sb);
+  r = s > 0.f ? __frcp_rn(s) : 0.f;
+  return bad ? 0x7fu : sb;
+}
+template <bool F32, bool NV>
+__device__ __forceinline__ float scaled(float x, float down, float s, float r) {
+  if (!NV) return x * r;
+  // x / s correctly rounded: one correction of the product with the correctly rounded
+  // reciprocal (P. Markstein, "Computation of elementary functions on the IBM RISC
+  // System/6000 processor", 1990).  a is x 2^-eg, exact.
+  const float a = x * down;
+  float t = a * r;
+  t = fmaf(fmaf(-t, s, a), r, t);
+  // a bf16 x and its quotient differ from every border or are on it: no remainder can hide
+  if (F32 && s > 0.f) t = odd(t, fmaf(-t, s, a), a);
+  return copysignf(t, a);   // the correction of -0 gives +0
+}
+
 // Codes (16 bytes) of 32 columns and their scale byte (MX) or two (NV: the second in bits 8-15).
 template <bool F32, bool NV>
-__device__ __forceinline__ uint32_t quantize32(const Cols32<F32> &v, int eg, uint32_t (&codes)[4]) {
+__device__ __forceinline__ uint32_t quantize32(const Cols32<F32> &v, float down, uint32_t (&codes)[4]) {
   uint32_t scales = 0;
-  if (!NV) {
-    const uint32_t top = v.template top<0, 32>();
-    const bool bad = top >= 0x7f800000u;
-    const uint32_t be = top >> 23;
-    const uint32_t s = be > 2 ? be - 2 : 0;            // biased exponent of the scale, 2^-127 at least
-    const float inv = __uint_as_float((254u - s) << 23);   // exact: a power of two
 #pragma unroll
-    for (int g = 0; g < 4; ++g) {
+  for (int h = 0; h < (NV ? 2 : 1); ++h) {
+    const uint32_t top = !NV ? v.template top<0, 32>() : h == 0 ? v.template top<0, 16>() : v.template top<16, 16>();
+    float s = 0.f, r;
+    scales |= block_scale<NV>(top, down, s, r) << (8 * h);
+#pragma unroll
+    for (int g = 0; g < (NV ? 2 : 4); ++g) {
       float x[8];
 #pragma unroll
-      for (int e = 0; e < 8; ++e) x[e] = v.get(8 * g + e) * inv;
+      for (int e = 0; e < 8; ++e) x[e] = scaled<F32, NV>(v.get(16 * h + 8 * g + e), down, s, r);
       const uint32_t c = e2m1x8(x);
-      codes[g] = bad ? 0u : c;
+      codes[2 * h + g] = top >= 0x7f800000u ? 0u : c;
     }
-    return bad ? 255u : s;
-  }
-  const float down = power_of_two(-eg);
-#pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    const uint32_t top = h == 0 ? v.template top<0, 16>() : v.template top<16, 16>();
-    const bool bad = top >= 0x7f800000u;
-    const float m = (bad ? 0.f : __uint_as_float(top)) * down;
-    const float q6 = __fdiv_rn(m, 6.f);
-    const uint32_t sb = to_e4m3(odd(q6, fmaf(-q6, 6.f, m), m));
-    const float s = from_e4m3(sb);
-    const float r = s > 0.f ? __frcp_rn(s) : 0.f;
-#pragma unroll
-    for (int g = 0; g < 2; ++g) {
-      float x[8];
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        // x / s correctly rounded: one correction of the product with the correctly rounded
-        // reciprocal (P. Markstein, "Computation of elementary functions on the IBM RISC
-        // System/6000 processor", 1990).  x is x 2^-eg, exact.
-        const float a = v.get(16 * h + 8 * g + e) * down;
-        float t = a * r;
-        t = fmaf(fmaf(-t, s, a), r, t);
-        // a bf16 x and its quotient differ from every border or are on it: no remainder can hide
-        if (F32 && s > 0.f) t = odd(t, fmaf(-t, s, a), a);
-        x[e] = copysignf(t, a);   // the correction of -0 gives +0
-      }
-      const uint32_t c = e2m1x8(x);
-      codes[2 * h + g] = bad ? 0u : c;
-    }
-    scales |= (bad ? 0x7fu : sb) << (8 * h);
   }
   return scales;
 }
@@ -223,190 +250,329 @@ __device__ __forceinline__ void load_cols(const void *x, int64_t off, int c, int
   }
 }
 
-template <bool F32, bool NV>
-__device__ __forceinline__ void quantize_tile(const Fp4Item &q, int tr, int tk, int eg, uint8_t *stage) {
-  const int kc = threadIdx.x & 3, r0 = threadIdx.x >> 2;
-  Cols32<F32> v[2];
+// A tile of the launch's list: its item, its row and column among the item's tiles.
+struct Tile {
+  int item, l, tr, tk;
+};
+template <class P>
+__device__ __forceinline__ Tile tile_at(const P &p, int t) {
+  Tile r;
+  r.item = find_item(p, t);
+  r.l = t - p.item[r.item].tile_begin;
+  r.tr = r.l / p.item[r.item].ktiles;
+  r.tk = r.l - r.tr * p.item[r.item].ktiles;
+  return r;
+}
+
+// NVFP4: 2^-e of an item's scale, from the records of the pass before (every CTA for itself); its first tile's
+// CTA writes the scale.
+template <class P>
+__device__ float down_of(const P &p, const Fp4Item &q, bool write) {
+  __shared__ uint32_t tops[kThreads / 32];
+  uint32_t top = 0;
+  for (int i = threadIdx.x; i < q.n_rec; i += kThreads) top = max(top, (uint32_t)p.rec[q.rec_begin + i]);
+  top = __reduce_max_sync(0xffffffffu, top);
+  __syncthreads();
+  if ((threadIdx.x & 31) == 0) tops[threadIdx.x >> 5] = top;
+  __syncthreads();
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const int row = tr * kT + r0 + 64 * i;
-    load_cols<F32, 32>(q.x, (int64_t)row * q.ld, tk * kT + kc * 32, q.cols, q.flags & kFp4Vec, row < q.rows, v[i].w);
-  }
+  for (int w = 0; w < kThreads / 32; ++w) top = max(top, tops[w]);
+  const int eg = global_exponent(top);
+  if (write && threadIdx.x == 0) *q.global = power_of_two(eg);
+  return power_of_two(-eg);
+}
+
+template <bool NV>
+__device__ __forceinline__ void store_scales(const Fp4Item &q, int l, const uint8_t *stage) {
+  constexpr int kBytes = NV ? 1024 : 512;
+  if (threadIdx.x * 4 < kBytes)
+    reinterpret_cast<uint32_t *>(q.scales + (int64_t)l * kBytes)[threadIdx.x] = reinterpret_cast<const uint32_t *>(stage)[threadIdx.x];
+}
+
+template <bool F32, bool NV, int N>
+__global__ void __launch_bounds__(kThreads, 4) fp4_quantize_kernel(const __grid_constant__ Fp4Block<N> p) {
+  constexpr int kBatch = F32 ? 2 : 4;                    // rows of a lane in a batch: 64 bytes
+  __shared__ __align__(16) uint8_t stage[2][1024];
+  pdl_trigger();
+  pdl_wait();
+  const int l = threadIdx.x & 15, r0 = threadIdx.x >> 4;
+  auto load = [&](const Tile &t, int b, Cols8<F32> (&v)[kBatch]) {
+    const Fp4Item &q = p.item[t.item];
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    uint32_t codes[4];
-    const uint32_t s = quantize32<F32, NV>(v[i], eg, codes);
-    put<NV>(q, tr, tk, r0 + 64 * i, kc, codes, s, stage);
+    for (int i = 0; i < kBatch; ++i) {
+      const int row = t.tr * kT + r0 + 16 * (b + i);
+      load_cols<F32, 8>(q.x, (int64_t)row * q.ld, t.tk * kT + 8 * l, q.cols, q.flags & kFp4Vec, row < q.rows, v[i].w);
+    }
+  };
+  int at_tile = blockIdx.x, last_item = -1, turn = 0;
+  if (at_tile >= p.total_tiles) return;
+  Tile t = tile_at(p, at_tile);
+  Cols8<F32> next[kBatch];
+  load(t, 0, next);
+  float down = 1.f;
+  for (;;) {
+    const Fp4Item &q = p.item[t.item];
+    if (NV && (t.item != last_item || t.l == 0)) {
+      down = down_of(p, q, t.l == 0);
+      last_item = t.item;
+    }
+    const int next_tile = at_tile + gridDim.x;
+    const bool more = next_tile < p.total_tiles;
+    const Tile tn = more ? tile_at(p, next_tile) : t;
+#pragma unroll
+    for (int b = 0; b < 8; b += kBatch) {
+      Cols8<F32> v[kBatch];
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) v[i] = next[i];
+      if (b + kBatch < 8) load(t, b + kBatch, next);
+      else if (more) load(tn, 0, next);
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) {
+        const int r = r0 + 16 * (b + i), row = t.tr * kT + r;
+        // a block is two lanes (NV) or four
+        uint32_t top = v[i].top();
+        top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+        if (!NV) top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+        float s = 0.f, rc, x[8];
+        const uint32_t sb = block_scale<NV>(top, down, s, rc);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[e] = scaled<F32, NV>(v[i].get(e), down, s, rc);
+        const uint32_t c = e2m1x8(x);
+        if (row < q.rows)
+          *reinterpret_cast<uint32_t *>(q.codes + (int64_t)row * q.ktiles * 64 + t.tk * 64 + 4 * l) = top >= 0x7f800000u ? 0u : c;
+        const int at = 16 * (r & 31) + 4 * (r >> 5);
+        if (NV) {
+          if ((l & 1) == 0) stage[turn][(l >> 3) * 512 + at + ((l >> 1) & 3)] = (uint8_t)sb;
+        } else {
+          if ((l & 3) == 0) stage[turn][at + (l >> 2)] = (uint8_t)sb;
+        }
+      }
+    }
+    __syncthreads();       // the other half of the stage is free again after this one
+    store_scales<NV>(q, t.l, stage[turn]);
+    turn ^= 1;
+    if (!more) break;
+    t = tn;
+    at_tile = next_tile;
   }
 }
 
-// The tile of the source: rows tk * 128 .. (the 4-bit matrix's columns), columns tr * 128 ...
-template <bool F32, bool NV>
-__device__ __forceinline__ void quantize_tile_t(const Fp4Item &q, int tr, int tk, int eg, uint8_t *stage, uint32_t *tile) {
+// The transpose.  A tile of the source: rows tk * 128 .. (the 4-bit matrix's columns), columns tr * 128 ...
+template <bool F32, bool NV, int N>
+__global__ void __launch_bounds__(kThreads, F32 ? 2 : 3) fp4_quantize_t_kernel(const __grid_constant__ Fp4Block<N> p) {
+  extern __shared__ uint32_t tile[];
+  __shared__ __align__(16) uint8_t stage[2][1024];
+  pdl_trigger();
+  pdl_wait();
   constexpr int WPR = F32 ? 128 : 64;            // words per row of the tile
   constexpr int TPR = WPR / 4;                   // threads per row, 16 bytes each
+  constexpr int kLoads = kT * TPR / kThreads;
+  const int lr = (int)threadIdx.x / TPR, lw = 4 * ((int)threadIdx.x % TPR);
+  struct Piece {
+    uint32_t w[4];
+  };
+  auto load = [&](const Tile &t, Piece (&v)[kLoads]) {
+    const Fp4Item &q = p.item[t.item];
 #pragma unroll
-  for (int i = 0; i < kT * TPR / kThreads; ++i) {
-    const int r = (int)threadIdx.x / TPR + i * (kThreads / TPR), w = 4 * ((int)threadIdx.x % TPR);
-    const int row = tk * kT + r;
-    uint32_t v[4];
-    load_cols<F32, F32 ? 4 : 8>(q.x, (int64_t)row * q.ld, tr * kT + (F32 ? w : 2 * w), q.rows, q.flags & kFp4Vec,
-                                row < q.cols, v);
-    *reinterpret_cast<uint4 *>(tile + r * WPR + (w ^ ((r >> 5) << 3))) = make_uint4(v[0], v[1], v[2], v[3]);
-  }
-  __syncthreads();
-  const int kc = threadIdx.x & 3, c0 = threadIdx.x >> 2;
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    // fp32: columns c0 and c0 + 64; bf16: the two columns of word c0
-    const int c = F32 ? c0 + 64 * i : 2 * c0 + i, word = F32 ? c : c0;
-    Cols32<F32> v;
-#pragma unroll
-    for (int e = 0; e < 32; e += 2) {
-      const uint32_t a = tile[(kc * 32 + e) * WPR + (word ^ (kc << 3))];
-      const uint32_t b = tile[(kc * 32 + e + 1) * WPR + (word ^ (kc << 3))];
-      if (F32) {
-        v.w[F32 ? e : 0] = a;
-        v.w[F32 ? e + 1 : 0] = b;
-      } else {
-        v.w[e / 2] = __byte_perm(a, b, i == 0 ? 0x5410 : 0x7632);
-      }
+    for (int i = 0; i < kLoads; ++i) {
+      const int row = t.tk * kT + lr + i * (kThreads / TPR);
+      load_cols<F32, F32 ? 4 : 8>(q.x, (int64_t)row * q.ld, t.tr * kT + (F32 ? lw : 2 * lw), q.rows, q.flags & kFp4Vec,
+                                  row < q.cols, v[i].w);
     }
-    uint32_t codes[4];
-    const uint32_t s = quantize32<F32, NV>(v, eg, codes);
-    put<NV>(q, tr, tk, c, kc, codes, s, stage);
-  }
-}
-
-template <bool TRANS, int N>
-__global__ void __launch_bounds__(kThreads) fp4_quantize_kernel(const __grid_constant__ Fp4Block<N> p) {
-  extern __shared__ uint32_t tile[];
-  __shared__ __align__(16) uint8_t stage[1024];
-  __shared__ uint32_t tops[kThreads / 32];
-  pdl_trigger();
-  pdl_wait();
-  const Fp4Item &q = p.item[find_item(p, blockIdx.x)];
-  const int l = blockIdx.x - q.tile_begin, tr = l / q.ktiles, tk = l - tr * q.ktiles;
-  const bool nv = q.flags & kFp4Nv, f32 = q.flags & kFp4F32;
-  int eg = 0;
-  if (nv) {
-    // the largest magnitude, from the records of the pass before (every CTA for itself)
-    uint32_t top = 0;
-    for (int i = threadIdx.x; i < q.n_rec; i += kThreads) top = max(top, (uint32_t)p.rec[q.rec_begin + i]);
-    top = __reduce_max_sync(0xffffffffu, top);
-    if ((threadIdx.x & 31) == 0) tops[threadIdx.x >> 5] = top;
+  };
+  int at_tile = blockIdx.x, last_item = -1, turn = 0;
+  if (at_tile >= p.total_tiles) return;
+  Tile t = tile_at(p, at_tile);
+  Piece next[kLoads];
+  load(t, next);
+  float down = 1.f;
+  for (;;) {
+    const Fp4Item &q = p.item[t.item];
+    if (NV && (t.item != last_item || t.l == 0)) {
+      down = down_of(p, q, t.l == 0);
+      last_item = t.item;
+    }
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i) {
+      const int r = lr + i * (kThreads / TPR);
+      *reinterpret_cast<uint4 *>(tile + r * WPR + (lw ^ ((r >> 5) << 3))) =
+          make_uint4(next[i].w[0], next[i].w[1], next[i].w[2], next[i].w[3]);
+    }
     __syncthreads();
+    const int next_tile = at_tile + gridDim.x;
+    const bool more = next_tile < p.total_tiles;
+    const Tile tn = more ? tile_at(p, next_tile) : t;
+    if (more) load(tn, next);
+    const int kc = threadIdx.x & 3, c0 = threadIdx.x >> 2;
 #pragma unroll
-    for (int w = 0; w < kThreads / 32; ++w) top = max(top, tops[w]);
-    eg = global_exponent(top);
-    if (l == 0 && threadIdx.x == 0) *q.global = power_of_two(eg);
+    for (int i = 0; i < 2; ++i) {
+      // fp32: columns c0 and c0 + 64; bf16: the two columns of word c0
+      const int c = F32 ? c0 + 64 * i : 2 * c0 + i, word = F32 ? c : c0;
+      Cols32<F32> v;
+#pragma unroll
+      for (int e = 0; e < 32; e += 2) {
+        const uint32_t a = tile[(kc * 32 + e) * WPR + (word ^ (kc << 3))];
+        const uint32_t b = tile[(kc * 32 + e + 1) * WPR + (word ^ (kc << 3))];
+        if (F32) {
+          v.w[F32 ? e : 0] = a;
+          v.w[F32 ? e + 1 : 0] = b;
+        } else {
+          v.w[e / 2] = __byte_perm(a, b, i == 0 ? 0x5410 : 0x7632);
+        }
+      }
+      uint32_t codes[4];
+      const uint32_t s = quantize32<F32, NV>(v, down, codes);
+      put<NV>(q, t.tr, t.tk, c, kc, codes, s, stage[turn]);
+    }
+    __syncthreads();       // the tile may be overwritten, the scales are staged
+    store_scales<NV>(q, t.l, stage[turn]);
+    turn ^= 1;
+    if (!more) break;
+    t = tn;
+    at_tile = next_tile;
   }
-  if (TRANS) {
-    if (nv) f32 ? quantize_tile_t<true, true>(q, tr, tk, eg, stage, tile) : quantize_tile_t<false, true>(q, tr, tk, eg, stage, tile);
-    else f32 ? quantize_tile_t<true, false>(q, tr, tk, eg, stage, tile) : quantize_tile_t<false, false>(q, tr, tk, eg, stage, tile);
-  } else {
-    if (nv) f32 ? quantize_tile<true, true>(q, tr, tk, eg, stage) : quantize_tile<false, true>(q, tr, tk, eg, stage);
-    else f32 ? quantize_tile<true, false>(q, tr, tk, eg, stage) : quantize_tile<false, false>(q, tr, tk, eg, stage);
-  }
-  __syncthreads();
-  const int bytes = nv ? 1024 : 512;
-  if (threadIdx.x * 4 < bytes)
-    reinterpret_cast<uint32_t *>(q.scales + (int64_t)l * bytes)[threadIdx.x] = reinterpret_cast<uint32_t *>(stage)[threadIdx.x];
 }
 
-// Values of 32 columns, two rows a thread.
-template <int N>
-__global__ void __launch_bounds__(kThreads) fp4_dequantize_kernel(const __grid_constant__ Fp4Block<N> p) {
+template <bool F32, bool NV, int N>
+__global__ void __launch_bounds__(kThreads, 4) fp4_dequantize_kernel(const __grid_constant__ Fp4Block<N> p) {
+  __shared__ __align__(16) float stage[(kThreads / 32) * 2 * kT];
   pdl_trigger();
   pdl_wait();
-  const Fp4Item &q = p.item[find_item(p, blockIdx.x)];
-  const int l = blockIdx.x - q.tile_begin, tr = l / q.ktiles, tk = l - tr * q.ktiles;
-  const bool nv = q.flags & kFp4Nv, f32 = q.flags & kFp4F32;
-  const int kc = threadIdx.x & 3;
-  const float g = nv ? *q.global : 1.f;
+  const int l = threadIdx.x & 15, r0 = threadIdx.x >> 4, lane = threadIdx.x & 31;
+  struct Codes {
+    uint32_t code[8], scale[8];
+    float g;
+  };
+  auto load = [&](const Tile &t, Codes &v) {
+    const Fp4Item &q = p.item[t.item];
+    v.g = NV ? *q.global : 1.f;
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const int r = (threadIdx.x >> 2) + 64 * i, row = tr * kT + r;
-    const int c = tk * kT + kc * 32;
-    if (row >= q.rows || c >= q.cols) continue;
-    const uint4 u = *reinterpret_cast<const uint4 *>(q.codes + (int64_t)row * q.ktiles * 64 + tk * 64 + kc * 16);
-    const int at = 16 * (r & 31) + 4 * (r >> 5);
-    float s0, s1;
-    if (nv) {
-      const uint32_t b = *reinterpret_cast<const unsigned short *>(q.scales + (int64_t)l * 1024 + (kc >> 1) * 512 + at + 2 * (kc & 1));
-      s0 = from_e4m3(b & 0xffu);
-      s1 = from_e4m3(b >> 8);
-    } else {
-      s0 = s1 = from_e8m0(q.scales[(int64_t)l * 512 + at + kc]);
-    }
-    const uint32_t cw[4] = {u.x, u.y, u.z, u.w};
-    float y[32];
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      float x[8];
-      e2m1x8_to_f32(cw[e], x);
-#pragma unroll
-      for (int k = 0; k < 8; ++k) y[8 * e + k] = x[k] * (e < 2 ? s0 : s1) * g;
-    }
-    const bool whole = (q.flags & kFp4Vec) && c + 32 <= q.cols;
-    if (f32) {
-      float *d = static_cast<float *>(q.x) + (int64_t)row * q.ld + c;
-      if (whole) {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) reinterpret_cast<float4 *>(d)[e] = make_float4(y[4 * e], y[4 * e + 1], y[4 * e + 2], y[4 * e + 3]);
-      } else {
-#pragma unroll
-        for (int e = 0; e < 32; ++e)
-          if (c + e < q.cols) d[e] = y[e];
-      }
-    } else {
-      __nv_bfloat16 *d = static_cast<__nv_bfloat16 *>(q.x) + (int64_t)row * q.ld + c;
-      if (whole) {
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-          reinterpret_cast<uint4 *>(d)[e] = make_uint4(pack_bf16(y[8 * e], y[8 * e + 1]), pack_bf16(y[8 * e + 2], y[8 * e + 3]),
-                                                       pack_bf16(y[8 * e + 4], y[8 * e + 5]), pack_bf16(y[8 * e + 6], y[8 * e + 7]));
-      } else {
-#pragma unroll
-        for (int e = 0; e < 32; ++e)
-          if (c + e < q.cols) d[e] = __float2bfloat16_rn(y[e]);
+    for (int i = 0; i < 8; ++i) {
+      const int r = r0 + 16 * i, row = t.tr * kT + r;
+      const int at = 16 * (r & 31) + 4 * (r >> 5);
+      v.code[i] = v.scale[i] = 0;
+      if (row < q.rows) {
+        v.code[i] = *reinterpret_cast<const uint32_t *>(q.codes + (int64_t)row * q.ktiles * 64 + t.tk * 64 + 4 * l);
+        v.scale[i] = NV ? q.scales[(int64_t)t.l * 1024 + (l >> 3) * 512 + at + ((l >> 1) & 3)]
+                        : q.scales[(int64_t)t.l * 512 + at + (l >> 2)];
       }
     }
+  };
+  int at_tile = blockIdx.x;
+  if (at_tile >= p.total_tiles) return;
+  Tile t = tile_at(p, at_tile);
+  Codes next;
+  load(t, next);
+  for (;;) {
+    const Codes v = next;
+    const Fp4Item &q = p.item[t.item];
+    const int next_tile = at_tile + gridDim.x;
+    const bool more = next_tile < p.total_tiles;
+    const Tile tn = more ? tile_at(p, next_tile) : t;
+    if (more) load(tn, next);
+    const int c = t.tk * kT + 8 * l;
+    const bool rows_whole = (q.flags & kFp4Vec) && t.tk * kT + kT <= q.cols;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int row = t.tr * kT + r0 + 16 * i;
+      const float s = NV ? from_e4m3(v.scale[i]) : from_e8m0(v.scale[i]);
+      float y[8];
+      e2m1x8_to_f32(v.code[i], y);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) y[e] = y[e] * s * v.g;
+      if (rows_whole) {
+        if (row >= q.rows) continue;
+        const int64_t at = (int64_t)row * q.ld + c;
+        if (F32) {
+          float4 *d = reinterpret_cast<float4 *>(static_cast<float *>(q.x) + at);
+          d[0] = make_float4(y[0], y[1], y[2], y[3]);
+          d[1] = make_float4(y[4], y[5], y[6], y[7]);
+        } else {
+          *reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(q.x) + at) =
+              make_uint4(pack_bf16(y[0], y[1]), pack_bf16(y[2], y[3]), pack_bf16(y[4], y[5]), pack_bf16(y[6], y[7]));
+        }
+      } else {
+        // through shared memory, so that a store instruction covers neighbouring elements
+        float *w = stage + (threadIdx.x >> 5) * 2 * kT;
+        __syncwarp();
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+          *reinterpret_cast<float4 *>(w + (lane >> 4) * kT + 8 * l + 4 * e) =
+              make_float4(y[4 * e], y[4 * e + 1], y[4 * e + 2], y[4 * e + 3]);
+        __syncwarp();
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const int rr = e >> 2, cc = 32 * (e & 3) + lane;
+          const int to_row = t.tr * kT + (r0 & ~1) + rr + 16 * i, to_col = t.tk * kT + cc;
+          if (to_row >= q.rows || to_col >= q.cols) continue;
+          const int64_t at = (int64_t)to_row * q.ld + to_col;
+          if (F32) static_cast<float *>(q.x)[at] = w[rr * kT + cc];
+          else static_cast<__nv_bfloat16 *>(q.x)[at] = __float2bfloat16_rn(w[rr * kT + cc]);
+        }
+      }
+    }
+    if (!more) break;
+    t = tn;
+    at_tile = next_tile;
   }
 }
 
 constexpr int kTileBytesT = kT * 128 * 4;   // an fp32 tile of the transposing kernel
 
-template <int N>
+int grid_of(int tiles, int per_sm) {
+  const int most = per_sm * device_sms();
+  return tiles < most ? tiles : most;
+}
+
+// The items of a launch are of one dtype and format.
+template <bool F32, bool NV, int N>
 cudaError_t launch_quantize(const Fp4Params &p, bool transpose, cudaStream_t s) {
   const Fp4Block<N> &b = prefix<Fp4Block<N>>(p);
-  if (!transpose) return launch_pdl(fp4_quantize_kernel<false, N>, dim3(p.total_tiles), dim3(kThreads), 0, s, b);
-  bool f32 = false;
-  for (int i = 0; i < p.n; ++i) f32 = f32 || (p.item[i].flags & kFp4F32);
+  if (!transpose)
+    return launch_pdl(fp4_quantize_kernel<F32, NV, N>, dim3(grid_of(p.total_tiles, 4)), dim3(kThreads), 0, s, b);
+  const int smem = F32 ? kTileBytesT : kTileBytesT / 2;
   static PerDevice attr_set;
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
-  if (f32 && !attr_set.get(dev)) {
-    e = cudaFuncSetAttribute(fp4_quantize_kernel<true, N>, cudaFuncAttributeMaxDynamicSharedMemorySize, kTileBytesT);
+  if (!attr_set.get(dev)) {
+    e = cudaFuncSetAttribute(fp4_quantize_t_kernel<F32, NV, N>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
     attr_set.set(dev, 1);
   }
-  return launch_pdl(fp4_quantize_kernel<true, N>, dim3(p.total_tiles), dim3(kThreads), f32 ? kTileBytesT : kTileBytesT / 2, s, b);
+  return launch_pdl(fp4_quantize_t_kernel<F32, NV, N>, dim3(grid_of(p.total_tiles, F32 ? 2 : 3)), dim3(kThreads), smem, s, b);
+}
+template <bool F32, bool NV, int N>
+cudaError_t launch_dequantize(const Fp4Params &p, cudaStream_t s) {
+  return launch_pdl(fp4_dequantize_kernel<F32, NV, N>, dim3(grid_of(p.total_tiles, 4)), dim3(kThreads), 0, s,
+                    prefix<Fp4Block<N>>(p));
+}
+
+// Calls f(F32, NV, N) for a launch's dtype, format and the smallest instance that holds its items.
+template <class F>
+cudaError_t with_kind(const Fp4Params &p, F &&f) {
+  const bool f32 = p.item[0].flags & kFp4F32, nv = p.item[0].flags & kFp4Nv;
+  auto n = [&](auto a, auto b) {
+    return p.n <= kFewFp4 ? f(a, b, std::integral_constant<int, kFewFp4>()) : f(a, b, std::integral_constant<int, kMaxFp4>());
+  };
+  if (f32) return nv ? n(std::true_type(), std::true_type()) : n(std::true_type(), std::false_type());
+  return nv ? n(std::false_type(), std::true_type()) : n(std::false_type(), std::false_type());
 }
 
 }  // namespace
 
 cudaError_t launch_fp4_quantize(const Fp4Params &p, bool transpose, cudaStream_t s) {
   if (p.total_tiles <= 0) return cudaSuccess;
-  return p.n <= kFewFp4 ? launch_quantize<kFewFp4>(p, transpose, s) : launch_quantize<kMaxFp4>(p, transpose, s);
+  return with_kind(p, [&](auto f32, auto nv, auto n) {
+    return launch_quantize<decltype(f32)::value, decltype(nv)::value, decltype(n)::value>(p, transpose, s);
+  });
 }
 
 cudaError_t launch_fp4_dequantize(const Fp4Params &p, cudaStream_t s) {
   if (p.total_tiles <= 0) return cudaSuccess;
-  if (p.n <= kFewFp4)
-    return launch_pdl(fp4_dequantize_kernel<kFewFp4>, dim3(p.total_tiles), dim3(kThreads), 0, s, prefix<Fp4Block<kFewFp4>>(p));
-  return launch_pdl(fp4_dequantize_kernel<kMaxFp4>, dim3(p.total_tiles), dim3(kThreads), 0, s, p);
+  return with_kind(p, [&](auto f32, auto nv, auto n) {
+    return launch_dequantize<decltype(f32)::value, decltype(nv)::value, decltype(n)::value>(p, s);
+  });
 }
 
 }  // namespace nshb

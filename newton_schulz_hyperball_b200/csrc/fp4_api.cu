@@ -44,6 +44,12 @@ bool fill_item(const nshb_fp4 &q, const nshb_tensor &x, int64_t &tiles, Fp4Item 
   return true;
 }
 
+// Whether an item's launch has to be another one than `first`'s.
+bool another_kind(const nshb_tensor &x, const nshb_fp4 &q, const Fp4Item &first) {
+  const int kind = (x.dtype == NSHB_F32 ? kFp4F32 : 0) | (q.format == NSHB_NVFP4 ? kFp4Nv : 0);
+  return kind != (first.flags & (kFp4F32 | kFp4Nv));
+}
+
 nshb_status check_pairs(const nshb_tensor *x, const nshb_fp4 *q, int32_t n, bool transpose) {
   const nshb_status e = check_tensors(x, n);
   if (e != NSHB_OK) return e;
@@ -220,6 +226,7 @@ nshb_status nshb_fp4_quantize(const nshb_tensor *X, const nshb_fp4 *Q, int32_t n
     int64_t tiles = 0;
     for (; i < n && p.n < kMaxFp4; ++i) {
       if (Q[i].rows == 0 || Q[i].cols == 0) continue;
+      if (p.n && another_kind(X[i], Q[i], p.item[0])) break;
       if (!fill_item(Q[i], X[i], tiles, p.item[p.n])) {
         if (p.n == 0) return NSHB_ERR_UNSUPPORTED;
         break;
@@ -256,6 +263,7 @@ nshb_status nshb_fp4_dequantize(const nshb_fp4 *Q, const nshb_tensor *X, int32_t
     int64_t tiles = 0;
     for (; i < n && p.n < kMaxFp4; ++i) {
       if (Q[i].rows == 0 || Q[i].cols == 0) continue;
+      if (p.n && another_kind(X[i], Q[i], p.item[0])) break;
       if (!fill_item(Q[i], X[i], tiles, p.item[p.n])) {
         if (p.n == 0) return NSHB_ERR_UNSUPPORTED;
         break;
