@@ -91,6 +91,18 @@ __device__ __forceinline__ int global_exponent(uint32_t top) {
   return e < -126 ? -126 : e;
 }
 
+// The larger magnitudes of two pairs of bf16 (NaN the largest), one instruction.
+__device__ __forceinline__ uint32_t max_magnitude(uint32_t m, uint32_t w) {
+  uint32_t r;
+  asm("{\n\t.reg .b32 a;\n\tabs.bf16x2 a, %2;\n\tmax.NaN.bf16x2 %0, %1, a;\n\t}" : "=r"(r) : "r"(m), "r"(w));
+  return r;
+}
+__device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+
 // 32 consecutive columns as they were loaded.
 template <bool F32>
 struct Cols32 {
@@ -110,7 +122,7 @@ struct Cols32 {
       return m;
     } else {
 #pragma unroll
-      for (int e = C / 2; e < (C + N) / 2; ++e) m = __vmaxu2(m, w[e] & 0x7fff7fffu);
+      for (int e = C / 2; e < (C + N) / 2; ++e) m = max_magnitude(m, w[e]);
       return max(m << 16, m & 0xffff0000u);
     }
   }
@@ -133,7 +145,7 @@ struct Cols8 {
       return m;
     } else {
 #pragma unroll
-      for (int e = 0; e < 4; ++e) m = __vmaxu2(m, w[e] & 0x7fff7fffu);
+      for (int e = 0; e < 4; ++e) m = max_magnitude(m, w[e]);
       return max(m << 16, m & 0xffff0000u);
     }
   }
@@ -171,6 +183,27 @@ __device__ __forceinline__ float scaled(float x, float down, float s, float r) {
   return copysignf(t, a);   // the correction of -0 gives +0
 }
 
+// The codes of 8 columns (words W .. of v).
+template <bool F32, bool NV, class V>
+__device__ __forceinline__ uint32_t codes8(const V &v, int first, uint32_t top, float down, float s, float r) {
+  float x[8];
+  if constexpr (!F32 && !NV) {
+    // bf16 times a power of two: exact in bf16 (what underflows is far below half a code)
+    const uint32_t r2 = (__float_as_uint(r) >> 16) | (__float_as_uint(r) & 0xffff0000u);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const uint32_t y = mul_bf16x2(v.w[first / 2 + e], r2);
+      x[2 * e] = bf16lo(y);
+      x[2 * e + 1] = bf16hi(y);
+    }
+  } else {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) x[e] = scaled<F32, NV>(v.get(first + e), down, s, r);
+  }
+  const uint32_t c = e2m1x8(x);
+  return top >= 0x7f800000u ? 0u : c;
+}
+
 // Codes (16 bytes) of 32 columns and their scale byte (MX) or two (NV: the second in bits 8-15).
 template <bool F32, bool NV>
 __device__ __forceinline__ uint32_t quantize32(const Cols32<F32> &v, float down, uint32_t (&codes)[4]) {
@@ -181,13 +214,7 @@ __device__ __forceinline__ uint32_t quantize32(const Cols32<F32> &v, float down,
     float s = 0.f, r;
     scales |= block_scale<NV>(top, down, s, r) << (8 * h);
 #pragma unroll
-    for (int g = 0; g < (NV ? 2 : 4); ++g) {
-      float x[8];
-#pragma unroll
-      for (int e = 0; e < 8; ++e) x[e] = scaled<F32, NV>(v.get(16 * h + 8 * g + e), down, s, r);
-      const uint32_t c = e2m1x8(x);
-      codes[2 * h + g] = top >= 0x7f800000u ? 0u : c;
-    }
+    for (int g = 0; g < (NV ? 2 : 4); ++g) codes[2 * h + g] = codes8<F32, NV>(v, 16 * h + 8 * g, top, down, s, r);
   }
   return scales;
 }
@@ -296,7 +323,36 @@ __global__ void __launch_bounds__(kThreads, 4) fp4_quantize_kernel(const __grid_
   pdl_trigger();
   pdl_wait();
   const int l = threadIdx.x & 15, r0 = threadIdx.x >> 4;
-  auto load = [&](const Tile &t, int b, Cols8<F32> (&v)[kBatch]) {
+  // This thread's first row of a tile: source, codes, and the way to the row 16 below.
+  struct Mine {
+    const char *src;
+    uint8_t *codes;
+    int64_t src_step;
+    int code_step;
+    bool whole;            // the tile has 128 rows and columns and its rows take 16-byte loads
+  };
+  auto mine = [&](const Tile &t) {
+    const Fp4Item &q = p.item[t.item];
+    Mine m;
+    const int64_t row = t.tr * kT + r0;
+    m.src = static_cast<const char *>(q.x) + (row * q.ld + t.tk * kT + 8 * l) * (F32 ? 4 : 2);
+    m.src_step = 16 * q.ld * (F32 ? 4 : 2);
+    m.codes = q.codes + row * q.ktiles * 64 + t.tk * 64 + 4 * l;
+    m.code_step = 16 * 64 * q.ktiles;
+    m.whole = (q.flags & kFp4Vec) && t.tr * kT + kT <= q.rows && t.tk * kT + kT <= q.cols;
+    return m;
+  };
+  auto load = [&](const Tile &t, const Mine &m, int b, Cols8<F32> (&v)[kBatch]) {
+    if (m.whole) {
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i)
+#pragma unroll
+        for (int g = 0; g < Cols8<F32>::NW / 4; ++g) {
+          const uint4 u = *reinterpret_cast<const uint4 *>(m.src + (b + i) * m.src_step + 16 * g);
+          v[i].w[4 * g] = u.x; v[i].w[4 * g + 1] = u.y; v[i].w[4 * g + 2] = u.z; v[i].w[4 * g + 3] = u.w;
+        }
+      return;
+    }
     const Fp4Item &q = p.item[t.item];
 #pragma unroll
     for (int i = 0; i < kBatch; ++i) {
@@ -307,8 +363,9 @@ __global__ void __launch_bounds__(kThreads, 4) fp4_quantize_kernel(const __grid_
   int at_tile = blockIdx.x, last_item = -1, turn = 0;
   if (at_tile >= p.total_tiles) return;
   Tile t = tile_at(p, at_tile);
+  Mine m = mine(t);
   Cols8<F32> next[kBatch];
-  load(t, 0, next);
+  load(t, m, 0, next);
   float down = 1.f;
   for (;;) {
     const Fp4Item &q = p.item[t.item];
@@ -319,33 +376,29 @@ __global__ void __launch_bounds__(kThreads, 4) fp4_quantize_kernel(const __grid_
     const int next_tile = at_tile + gridDim.x;
     const bool more = next_tile < p.total_tiles;
     const Tile tn = more ? tile_at(p, next_tile) : t;
+    const Mine mn = more ? mine(tn) : m;
+    // scale (r, b) of the tile is byte 16 (r mod 32) + 4 (r div 32) + b; r = r0 + 16 k
+    uint8_t *scale = stage[turn] + 16 * r0 + (NV ? (l >> 3) * 512 + ((l >> 1) & 3) : l >> 2);
+    const int rows_left = m.whole ? kT : q.rows - t.tr * kT - r0;
 #pragma unroll
     for (int b = 0; b < 8; b += kBatch) {
       Cols8<F32> v[kBatch];
 #pragma unroll
       for (int i = 0; i < kBatch; ++i) v[i] = next[i];
-      if (b + kBatch < 8) load(t, b + kBatch, next);
-      else if (more) load(tn, 0, next);
+      if (b + kBatch < 8) load(t, m, b + kBatch, next);
+      else if (more) load(tn, mn, 0, next);
 #pragma unroll
       for (int i = 0; i < kBatch; ++i) {
-        const int r = r0 + 16 * (b + i), row = t.tr * kT + r;
+        const int k = b + i;
         // a block is two lanes (NV) or four
         uint32_t top = v[i].top();
         top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
         if (!NV) top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
-        float s = 0.f, rc, x[8];
+        float s = 0.f, rc;
         const uint32_t sb = block_scale<NV>(top, down, s, rc);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) x[e] = scaled<F32, NV>(v[i].get(e), down, s, rc);
-        const uint32_t c = e2m1x8(x);
-        if (row < q.rows)
-          *reinterpret_cast<uint32_t *>(q.codes + (int64_t)row * q.ktiles * 64 + t.tk * 64 + 4 * l) = top >= 0x7f800000u ? 0u : c;
-        const int at = 16 * (r & 31) + 4 * (r >> 5);
-        if (NV) {
-          if ((l & 1) == 0) stage[turn][(l >> 3) * 512 + at + ((l >> 1) & 3)] = (uint8_t)sb;
-        } else {
-          if ((l & 3) == 0) stage[turn][at + (l >> 2)] = (uint8_t)sb;
-        }
+        const uint32_t c = codes8<F32, NV>(v[i], 0, top, down, s, rc);
+        if (16 * k < rows_left) *reinterpret_cast<uint32_t *>(m.codes + (int64_t)k * m.code_step) = c;
+        if ((l & (NV ? 1 : 3)) == 0) scale[256 * (k & 1) + 4 * (k >> 1)] = (uint8_t)sb;
       }
     }
     __syncthreads();       // the other half of the stage is free again after this one
@@ -353,6 +406,7 @@ __global__ void __launch_bounds__(kThreads, 4) fp4_quantize_kernel(const __grid_
     turn ^= 1;
     if (!more) break;
     t = tn;
+    m = mn;
     at_tile = next_tile;
   }
 }
