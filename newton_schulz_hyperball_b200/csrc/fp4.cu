@@ -169,7 +169,7 @@ __device__ __forceinline__ uint32_t block_scale(uint32_t top, float down, float 
   r = s > 0.f ? __frcp_rn(s) : 0.f;
   return bad ? 0x7fu : sb;
 }
-template <bool F32, bool NV>
+template <bool NV>
 __device__ __forceinline__ float scaled(float x, float down, float s, float r) {
   if (!NV) return x * r;
   // x / s correctly rounded: one correction of the product with the correctly rounded
@@ -178,8 +178,7 @@ __device__ __forceinline__ float scaled(float x, float down, float s, float r) {
   const float a = x * down;
   float t = a * r;
   t = fmaf(fmaf(-t, s, a), r, t);
-  // a bf16 x and its quotient differ from every border or are on it: no remainder can hide
-  if (F32 && s > 0.f) t = odd(t, fmaf(-t, s, a), a);
+  if (s > 0.f) t = odd(t, fmaf(-t, s, a), a);
   return copysignf(t, a);   // the correction of -0 gives +0
 }
 
@@ -196,9 +195,21 @@ __device__ __forceinline__ uint32_t codes8(const V &v, int first, uint32_t top, 
       x[2 * e] = bf16lo(y);
       x[2 * e + 1] = bf16hi(y);
     }
+  } else if constexpr (!F32) {
+    // A bf16 a (8 bits) is the border of two codes (3 bits) times s (4 bits), or differs from it by 2^-8 of
+    // itself.  So a quotient that is at most 2^-19 too large and then cut to 12 bits is on the
+    // border exactly where a / s is, and on its side of it elsewhere.
+    const uint32_t d = __float_as_uint(down), d2 = (d >> 16) | (d & 0xffff0000u);
+    const float up = r * (1.f + 0x1p-20f);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const uint32_t a = mul_bf16x2(v.w[first / 2 + e], d2);   // exact: a power of two
+      x[2 * e] = __uint_as_float(__float_as_uint(bf16lo(a) * up) & 0xfffff000u);
+      x[2 * e + 1] = __uint_as_float(__float_as_uint(bf16hi(a) * up) & 0xfffff000u);
+    }
   } else {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) x[e] = scaled<F32, NV>(v.get(first + e), down, s, r);
+    for (int e = 0; e < 8; ++e) x[e] = scaled<NV>(v.get(first + e), down, s, r);
   }
   const uint32_t c = e2m1x8(x);
   return top >= 0x7f800000u ? 0u : c;
@@ -500,15 +511,16 @@ __global__ void __launch_bounds__(kThreads, 4) fp4_dequantize_kernel(const __gri
   auto load = [&](const Tile &t, Codes &v) {
     const Fp4Item &q = p.item[t.item];
     v.g = NV ? *q.global : 1.f;
+    // scale (r, b) of the tile is byte 16 (r mod 32) + 4 (r div 32) + b; r = r0 + 16 i
+    const uint8_t *scale = q.scales + (int64_t)t.l * (NV ? 1024 : 512) + 16 * r0 + (NV ? (l >> 3) * 512 + ((l >> 1) & 3) : l >> 2);
+    const uint8_t *codes = q.codes + (int64_t)(t.tr * kT + r0) * q.ktiles * 64 + t.tk * 64 + 4 * l;
+    const int rows_left = q.rows - t.tr * kT - r0;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      const int r = r0 + 16 * i, row = t.tr * kT + r;
-      const int at = 16 * (r & 31) + 4 * (r >> 5);
       v.code[i] = v.scale[i] = 0;
-      if (row < q.rows) {
-        v.code[i] = *reinterpret_cast<const uint32_t *>(q.codes + (int64_t)row * q.ktiles * 64 + t.tk * 64 + 4 * l);
-        v.scale[i] = NV ? q.scales[(int64_t)t.l * 1024 + (l >> 3) * 512 + at + ((l >> 1) & 3)]
-                        : q.scales[(int64_t)t.l * 512 + at + (l >> 2)];
+      if (16 * i < rows_left) {
+        v.code[i] = *reinterpret_cast<const uint32_t *>(codes + (int64_t)i * 1024 * q.ktiles);
+        v.scale[i] = scale[256 * (i & 1) + 4 * (i >> 1)];
       }
     }
   };
@@ -524,25 +536,25 @@ __global__ void __launch_bounds__(kThreads, 4) fp4_dequantize_kernel(const __gri
     const bool more = next_tile < p.total_tiles;
     const Tile tn = more ? tile_at(p, next_tile) : t;
     if (more) load(tn, next);
-    const int c = t.tk * kT + 8 * l;
+    const int rows_left = q.rows - t.tr * kT - r0;
+    char *d = static_cast<char *>(q.x) + ((int64_t)(t.tr * kT + r0) * q.ld + t.tk * kT + 8 * l) * (F32 ? 4 : 2);
+    const int64_t step = 16 * q.ld * (F32 ? 4 : 2);
     const bool rows_whole = (q.flags & kFp4Vec) && t.tk * kT + kT <= q.cols;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      const int row = t.tr * kT + r0 + 16 * i;
       const float s = NV ? from_e4m3(v.scale[i]) : from_e8m0(v.scale[i]);
       float y[8];
       e2m1x8_to_f32(v.code[i], y);
 #pragma unroll
       for (int e = 0; e < 8; ++e) y[e] = y[e] * s * v.g;
       if (rows_whole) {
-        if (row >= q.rows) continue;
-        const int64_t at = (int64_t)row * q.ld + c;
+        if (16 * i >= rows_left) continue;
         if (F32) {
-          float4 *d = reinterpret_cast<float4 *>(static_cast<float *>(q.x) + at);
-          d[0] = make_float4(y[0], y[1], y[2], y[3]);
-          d[1] = make_float4(y[4], y[5], y[6], y[7]);
+          float4 *o = reinterpret_cast<float4 *>(d + i * step);
+          o[0] = make_float4(y[0], y[1], y[2], y[3]);
+          o[1] = make_float4(y[4], y[5], y[6], y[7]);
         } else {
-          *reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(q.x) + at) =
+          *reinterpret_cast<uint4 *>(d + i * step) =
               make_uint4(pack_bf16(y[0], y[1]), pack_bf16(y[2], y[3]), pack_bf16(y[4], y[5]), pack_bf16(y[6], y[7]));
         }
       } else {
