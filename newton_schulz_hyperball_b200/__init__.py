@@ -62,7 +62,7 @@ def _device_arg(t, what: str, dtype=None, min_numel: int = 0) -> None:
     `dtype` and at least `min_numel` elements.  Raw pointers (ints) and None pass unchecked."""
     if t is None or isinstance(t, int):
         return
-    if t.device.type != "cuda":
+    if not t.is_cuda:
         raise ValueError(f"{what} must be a CUDA tensor")
     if dtype is not None and t.dtype != dtype:
         raise TypeError(f"{what} must be {dtype}, got {t.dtype}")
@@ -384,20 +384,27 @@ def _on(name, handle, others, stream, *args):
     """Calls the library's `name` with the device of `handle` (a tensors or fp4_matrices array) current, on
     `stream` or that device's current stream; `others` (name, tensor or array) have to be on it."""
     import torch
+    fn = getattr(_LIB or lib(), name)
     dev = _device_of(handle)
     if dev is None:
-        _check(getattr(lib(), name)(*args, _stream(stream)), name)
+        _check(fn(*args, _stream(stream)), name)
         return
+    index = dev.index
     for what, t in others:
-        d = getattr(t, "device", None) or _device_of(t)
-        if d is not None and d != dev:
-            raise ValueError(f"{what} is on {d}, the tensors on {dev}")
-    st = _current_stream(dev.index) if stream is None else _stream(stream)
-    if dev.index == torch.cuda.current_device():
-        _check(getattr(lib(), name)(*args, st), name)
-        return
-    with torch.cuda.device(dev):
-        _check(getattr(lib(), name)(*args, st), name)
+        if t is None or isinstance(t, (int, tuple)):
+            continue
+        d = getattr(t, "_device", None)           # an array; else a tensor
+        d = t.get_device() if d is None and hasattr(t, "get_device") else d and d.index
+        if d is not None and d != index:
+            raise ValueError(f"{what} is on cuda:{d}, the tensors on {dev}")
+    st = _current_stream(index) if stream is None else _stream(stream)
+    if index == torch.cuda.current_device():
+        status = fn(*args, st)
+    else:
+        with torch.cuda.device(dev):
+            status = fn(*args, st)
+    if status:
+        _check(status, name)
 
 
 def grad_norm(g, total, ws, max_norm: float = float("inf"), each=None, kind: int = NSHB_NORM_L2, stream=None):

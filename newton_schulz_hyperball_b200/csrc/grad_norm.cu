@@ -7,6 +7,9 @@
 // the scaling.  All tensors of a launch form one line of 16 KB windows, split evenly over the
 // CTAs, so that a few vectors and a 12-million-element matrix cost their bytes alone; a CTA
 // keeps its sum in registers and reduces it only where its share of a tensor ends.
+//
+// Short lists are bound by launches: one cluster does all of a call, each CTA as four groups of 256 threads that
+// take the place of the CTAs of the long form (tens_small_kernel).
 #include <cuda_runtime.h>
 
 #include <type_traits>
@@ -17,7 +20,15 @@
 namespace nshb {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 256;   // of a group: a CTA of the long form, a quarter of one of the short form
+
+// The threads that work on one share of the line.
+struct Group {
+  int tid;             // 0 .. 255
+  int barrier;         // named barrier of the group
+  double *scratch;     // kThreads / 32 doubles
+  __device__ __forceinline__ void sync() const { named_barrier(barrier, kThreads); }
+};
 
 // The value of one kind over a set: a sum of squares, or the largest magnitude as its bit
 // pattern (magnitudes order as their bits; infinity and NaN are the largest).
@@ -28,22 +39,22 @@ __device__ __forceinline__ double warp_join(int kind, double v) {
   return v;
 }
 
-// Every thread gets the value of the whole block (fixed order); ends with the scratch free.
-__device__ __forceinline__ double block_join(int kind, double v, double *scratch) {
+// Every thread gets the value of the whole group (fixed order).
+__device__ __forceinline__ double group_join(int kind, double v, const Group &g) {
   v = warp_join(kind, v);
-  __syncthreads();
-  if ((threadIdx.x & 31) == 0) scratch[threadIdx.x >> 5] = v;
-  __syncthreads();
-  double s = scratch[0];
+  g.sync();
+  if ((g.tid & 31) == 0) g.scratch[g.tid >> 5] = v;
+  g.sync();
+  double s = g.scratch[0];
 #pragma unroll
-  for (int w = 1; w < kThreads / 32; ++w) s = join(kind, s, scratch[w]);
+  for (int w = 1; w < kThreads / 32; ++w) s = join(kind, s, g.scratch[w]);
   return s;
 }
 
-__device__ double join_records(int kind, const double *rec, int n, double *scratch) {
+__device__ double join_records(int kind, const double *rec, int n, const Group &g) {
   double v = 0.0;
-  for (int i = threadIdx.x; i < n; i += kThreads) v = join(kind, v, rec[i]);
-  return block_join(kind, v, scratch);
+  for (int i = g.tid; i < n; i += kThreads) v = join(kind, v, rec[i]);
+  return group_join(kind, v, g);
 }
 
 __device__ __forceinline__ float norm_of(int kind, double v) {
@@ -131,7 +142,7 @@ struct Place {
   bool whole;
 };
 template <bool F32>
-__device__ __forceinline__ Place place(const TensRec &q, int win) {
+__device__ __forceinline__ Place place(const TensRec &q, int win, int tid) {
   constexpr int E = Share<F32>::E, W = kWinBytes / (F32 ? 4 : 2);
   Place r;
   int k = win;
@@ -141,7 +152,7 @@ __device__ __forceinline__ Place place(const TensRec &q, int win) {
     k = win - r.row * q.per_row;
   }
   const uintptr_t base = reinterpret_cast<uintptr_t>(q.src) + (uintptr_t)((int64_t)r.row * q.sld * (F32 ? 4 : 2));
-  r.at = (int64_t)k * W - (int64_t)((base & 31) / (F32 ? 4 : 2)) + (int64_t)threadIdx.x * E;
+  r.at = (int64_t)k * W - (int64_t)((base & 31) / (F32 ? 4 : 2)) + (int64_t)tid * E;
   r.whole = r.at >= 0 && r.at + E <= q.cols;
   return r;
 }
@@ -150,8 +161,8 @@ __device__ __forceinline__ const char *run_ptr(const TensRec &q, const Place &l)
   return static_cast<const char *>(q.src) + ((int64_t)l.row * q.sld + l.at) * (F32 ? 4 : 2);
 }
 
-template <class V, bool F32>
-__device__ __forceinline__ double norm_windows(const TensRec &q, int w, int wend) {
+template <class V, bool F32, bool TWO>
+__device__ __forceinline__ double norm_windows(const TensRec &q, int w, int wend, int tid) {
   V v;
   if (q.flags & kTensRun) {
     auto add = [&](const Share<F32> &s) {
@@ -176,8 +187,8 @@ __device__ __forceinline__ double norm_windows(const TensRec &q, int w, int wend
       }
     };
     // two windows at a time: 128 bytes of each thread in flight
-    for (; w + 1 < wend; w += 2) {
-      const Place l0 = place<F32>(q, w), l1 = place<F32>(q, w + 1);
+    for (; TWO && w + 1 < wend; w += 2) {
+      const Place l0 = place<F32>(q, w, tid), l1 = place<F32>(q, w + 1, tid);
       if (l0.whole && l1.whole) {
         Share<F32> s0, s1;
         s0.load(run_ptr<F32>(q, l0));
@@ -189,12 +200,12 @@ __device__ __forceinline__ double norm_windows(const TensRec &q, int w, int wend
         one(l1);
       }
     }
-    if (w < wend) one(place<F32>(q, w));
+    for (; w < wend; ++w) one(place<F32>(q, w, tid));
   } else {
     for (; w < wend; ++w) {
       const int r0 = w * q.per_row, cols = (int)q.cols;
       const int nr = q.rows - r0 < q.per_row ? q.rows - r0 : q.per_row;
-      for (int i = threadIdx.x; i < nr * cols; i += kThreads) {
+      for (int i = tid; i < nr * cols; i += kThreads) {
         const int r = i / cols;
         v.add1(load1<F32>(q.src, (int64_t)(r0 + r) * q.sld + (i - r * cols)));
       }
@@ -218,10 +229,8 @@ __device__ __forceinline__ int find_tensor(const P &p, int win) {
 // tensor; where both borders meet it grows by two, and the record between is set to zero.  So the
 // records are a list without gaps in a fixed order, tensor t's are consecutive, and their number does
 // not depend on the sizes.
-template <class V, class P>
-__device__ __forceinline__ void norm_line(const P &p) {
-  __shared__ double scratch[kThreads / 32];
-  const int c = blockIdx.x;
+template <class V, bool TWO, class P>
+__device__ __forceinline__ void norm_line(const P &p, int c, const Group &g) {
   const int w0 = (int)((int64_t)c * p.nwin / p.nctas), w1 = (int)((int64_t)(c + 1) * p.nwin / p.nctas);
   int t = find_tensor(p, w0);
   for (int w = w0; w < w1; ++t) {
@@ -229,9 +238,9 @@ __device__ __forceinline__ void norm_line(const P &p) {
     const int tend = t + 1 < p.ntens ? p.t[t + 1].win_begin : p.nwin;
     const int wend = tend < w1 ? tend : w1;
     const int a = w - q.win_begin, b = wend - q.win_begin;
-    const double v = (q.flags & kTensF32) ? norm_windows<V, true>(q, a, b) : norm_windows<V, false>(q, a, b);
-    const double s = block_join(p.kind, v, scratch);
-    if (threadIdx.x == 0) {
+    const double v = (q.flags & kTensF32) ? norm_windows<V, true, TWO>(q, a, b, g.tid) : norm_windows<V, false, TWO>(q, a, b, g.tid);
+    const double s = group_join(p.kind, v, g);
+    if (g.tid == 0) {
       p.rec[c + t] = s;
       if (wend == tend && wend == w1 && t + 1 < p.ntens) p.rec[c + t + 1] = 0.0;
     }
@@ -239,58 +248,73 @@ __device__ __forceinline__ void norm_line(const P &p) {
   }
 }
 
-template <int N>
-__global__ void __launch_bounds__(kThreads, kNormCtasPerSm) tens_norm_kernel(const __grid_constant__ TensBlock<N> p) {
-  pdl_trigger();
-  pdl_wait();
-  if (p.kind == kNormL2) norm_line<SumSquares>(p);
-  else if (p.kind == kNormInf) norm_line<LargestBits<false>>(p);
-  else norm_line<LargestBits<true>>(p);
+template <bool TWO, class P>
+__device__ __forceinline__ void norm_share(const P &p, int c, const Group &g) {
+  if (p.kind == kNormL2) norm_line<SumSquares, TWO>(p, c, g);
+  else if (p.kind == kNormInf) norm_line<LargestBits<false>, TWO>(p, c, g);
+  else norm_line<LargestBits<true>, TWO>(p, c, g);
 }
 
-// One CTA: the norms of the tensors (where asked for) and of the whole.  A tensor's records are
-// summed by a thread where they are few, by a warp otherwise.
+template <int N>
+__global__ void __launch_bounds__(kThreads, kNormCtasPerSm) tens_norm_kernel(const __grid_constant__ TensBlock<N> p) {
+  __shared__ double scratch[kThreads / 32];
+  pdl_trigger();
+  pdl_wait();
+  norm_share<true>(p, blockIdx.x, Group{(int)threadIdx.x, 1, scratch});
+}
+
+// The norms of the tensors, from their records.  A tensor's records are summed by a thread where they are few, by
+// a warp otherwise.  at(k): first window and index of tensor k; the last n_empty have no elements.
+template <class At>
+__device__ __forceinline__ void norms_of_each(int kind, const double *rec, float *each, int ntens, int n_empty, int nwin,
+                                              int nctas, int tid, At &&at) {
+  const int lane = tid & 31;
+  for (int k0 = tid & ~31; k0 < ntens; k0 += kThreads) {
+    const int k = k0 + lane;
+    int c0 = 0, n = 0;
+    if (k < ntens) {
+      const int end = k + 1 < ntens ? at(k + 1).win_begin : nwin;
+      c0 = win_cta(at(k).win_begin, nwin, nctas);
+      n = win_cta(end - 1, nwin, nctas) - c0 + 1;
+    }
+    double v = 0.0;
+    if (n <= 8)
+      for (int i = 0; i < n; ++i) v = join(kind, v, rec[c0 + k + i]);
+    for (unsigned many = __ballot_sync(0xffffffffu, n > 8); many; many &= many - 1) {
+      const int src = __ffs(many) - 1;
+      const int first = __shfl_sync(0xffffffffu, c0 + k, src), count = __shfl_sync(0xffffffffu, n, src);
+      double s = 0.0;
+      for (int i = lane; i < count; i += 32) s = join(kind, s, rec[first + i]);
+      s = warp_join(kind, s);
+      if (lane == src) v = s;
+    }
+    if (k < ntens) each[at(k).index] = norm_of(kind, v);
+  }
+  for (int k = ntens + tid; k < ntens + n_empty; k += kThreads) each[at(k).index] = 0.f;
+}
+
+__device__ __forceinline__ float write_total(float *total, uint32_t *status, float norm, float max_norm) {
+  const float f = factor_of(norm, max_norm);
+  total[0] = norm;
+  total[1] = f;
+  *status = isfinite(norm) ? 0u : NSHB_DEV_NONFINITE;
+  return f;
+}
+
+// One CTA: the norms of the tensors (where asked for) and of the whole.
 template <int N>
 __global__ void __launch_bounds__(kThreads) tens_finalize_kernel(const __grid_constant__ TensFinBlock<N> p) {
   __shared__ double scratch[kThreads / 32];
   pdl_trigger();
   pdl_wait();
-  if (p.each) {
-    const int lane = threadIdx.x & 31;
-    for (int k0 = (int)(threadIdx.x & ~31u); k0 < p.ntens; k0 += kThreads) {
-      const int k = k0 + lane;
-      int c0 = 0, n = 0;
-      if (k < p.ntens) {
-        const int end = k + 1 < p.ntens ? p.at[k + 1].win_begin : p.nwin;
-        c0 = win_cta(p.at[k].win_begin, p.nwin, p.nctas);
-        n = win_cta(end - 1, p.nwin, p.nctas) - c0 + 1;
-      }
-      double v = 0.0;
-      if (n <= 8)
-        for (int i = 0; i < n; ++i) v = join(p.kind, v, p.rec[c0 + k + i]);
-      for (unsigned many = __ballot_sync(0xffffffffu, n > 8); many; many &= many - 1) {
-        const int src = __ffs(many) - 1;
-        const int first = __shfl_sync(0xffffffffu, c0 + k, src), count = __shfl_sync(0xffffffffu, n, src);
-        double s = 0.0;
-        for (int i = lane; i < count; i += 32) s = join(p.kind, s, p.rec[first + i]);
-        s = warp_join(p.kind, s);
-        if (lane == src) v = s;
-      }
-      if (k < p.ntens) p.each[p.at[k].index] = norm_of(p.kind, v);
-    }
-    for (int k = p.ntens + threadIdx.x; k < p.ntens + p.n_empty; k += kThreads) p.each[p.at[k].index] = 0.f;
-  }
-  double v = join_records(p.kind, p.rec, p.ntens ? p.nctas + p.ntens - 1 : 0, scratch);
+  if (p.each)
+    norms_of_each(p.kind, p.rec, p.each, p.ntens, p.n_empty, p.nwin, p.nctas, threadIdx.x,
+                  [&](int k) -> const TensPlace & { return p.at[k]; });
+  double v = join_records(p.kind, p.rec, p.ntens ? p.nctas + p.ntens - 1 : 0, Group{(int)threadIdx.x, 1, scratch});
   if (threadIdx.x == 0) {
     if (!p.first) v = join(p.kind, *p.acc, v);
-    if (!p.last) {
-      *p.acc = v;
-    } else {
-      const float norm = norm_of(p.kind, v);
-      p.total[0] = norm;
-      p.total[1] = factor_of(norm, p.max_norm);
-      *p.status = isfinite(norm) ? 0u : NSHB_DEV_NONFINITE;
-    }
+    if (!p.last) *p.acc = v;
+    else write_total(p.total, p.status, norm_of(p.kind, v), p.max_norm);
   }
 }
 
@@ -324,12 +348,12 @@ __device__ __forceinline__ void store_share(char *d, const float (&y)[E]) {
 }
 
 template <bool F32, bool DF32>
-__device__ __forceinline__ void scale_windows(const TensRec &q, int w, int wend, float f) {
+__device__ __forceinline__ void scale_windows(const TensRec &q, int w, int wend, float f, int tid) {
   constexpr int E = Share<F32>::E;
   // backwards: the windows that the norm read last are still in the L2 cache
   if (q.flags & kTensRun) {
     for (int u = wend - 1; u >= w; --u) {
-      const Place l = place<F32>(q, u);
+      const Place l = place<F32>(q, u, tid);
       char *drow = static_cast<char *>(q.dst) + (int64_t)l.row * q.dld * (DF32 ? 4 : 2);
       if (l.whole) {
         Share<F32> s;
@@ -348,11 +372,31 @@ __device__ __forceinline__ void scale_windows(const TensRec &q, int w, int wend,
     for (int u = wend - 1; u >= w; --u) {
       const int r0 = u * q.per_row, cols = (int)q.cols;
       const int nr = q.rows - r0 < q.per_row ? q.rows - r0 : q.per_row;
-      for (int i = threadIdx.x; i < nr * cols; i += kThreads) {
+      for (int i = tid; i < nr * cols; i += kThreads) {
         const int r = i / cols, j = i - r * cols;
         store1<DF32>(q.dst, (int64_t)(r0 + r) * q.dld + j, f * load1<F32>(q.src, (int64_t)(r0 + r) * q.sld + j));
       }
     }
+  }
+}
+
+template <class P>
+__device__ __forceinline__ void scale_share(const P &p, int c, float f, int tid) {
+  const int w0 = (int)((int64_t)c * p.nwin / p.nctas), w1 = (int)((int64_t)(c + 1) * p.nwin / p.nctas);
+  for (int t = find_tensor(p, w1 - 1), w = w1; w > w0; --t) {
+    const TensRec &q = p.t[t];
+    const int wb = q.win_begin > w0 ? q.win_begin : w0;
+    const int a = wb - q.win_begin, b = w - q.win_begin;
+    const bool still = f == 1.f && q.src == q.dst;   // in place: the values stay as they are
+    if (!still) {
+      switch (q.flags & (kTensF32 | kTensDstF32)) {
+        case 0: scale_windows<false, false>(q, a, b, f, tid); break;
+        case kTensF32: scale_windows<true, false>(q, a, b, f, tid); break;
+        case kTensDstF32: scale_windows<false, true>(q, a, b, f, tid); break;
+        default: scale_windows<true, true>(q, a, b, f, tid); break;
+      }
+    }
+    w = wb;
   }
 }
 
@@ -365,33 +409,40 @@ __global__ void __launch_bounds__(kThreads, kScaleCtasPerSm) tens_scale_kernel(c
   pdl_wait();
   float f;
   if (p.coef_rec) {
-    const float norm = norm_of(p.kind, join_records(p.kind, p.coef_rec, p.n_rec, scratch));
+    const float norm = norm_of(p.kind, join_records(p.kind, p.coef_rec, p.n_rec, Group{(int)threadIdx.x, 1, scratch}));
     f = factor_of(norm, p.max_norm);
-    if (blockIdx.x == 0 && threadIdx.x == 0) {
-      p.total[0] = norm;
-      p.total[1] = f;
-      *p.status = isfinite(norm) ? 0u : NSHB_DEV_NONFINITE;
-    }
+    if (blockIdx.x == 0 && threadIdx.x == 0) write_total(p.total, p.status, norm, p.max_norm);
   } else {
     f = *p.factor;
   }
-  const int c = blockIdx.x;
-  const int w0 = (int)((int64_t)c * p.nwin / p.nctas), w1 = (int)((int64_t)(c + 1) * p.nwin / p.nctas);
-  for (int t = find_tensor(p, w1 - 1), w = w1; w > w0; --t) {
-    const TensRec &q = p.t[t];
-    const int wb = q.win_begin > w0 ? q.win_begin : w0;
-    const int a = wb - q.win_begin, b = w - q.win_begin;
-    const bool still = f == 1.f && q.src == q.dst;   // in place: the values stay as they are
-    if (!still) {
-      switch (q.flags & (kTensF32 | kTensDstF32)) {
-        case 0: scale_windows<false, false>(q, a, b, f); break;
-        case kTensF32: scale_windows<true, false>(q, a, b, f); break;
-        case kTensDstF32: scale_windows<false, true>(q, a, b, f); break;
-        default: scale_windows<true, true>(q, a, b, f); break;
-      }
-    }
-    w = wb;
+  scale_share(p, blockIdx.x, f, threadIdx.x);
+}
+
+// All of a call on a short list: one cluster of kSmallCtas CTAs, four groups each.  The records cross between
+// the CTAs through the workspace, ordered by the cluster's barrier.
+constexpr int kSmallThreads = 4 * kThreads;
+__global__ void __launch_bounds__(kSmallThreads, 1) tens_small_kernel(const __grid_constant__ TensSmallParams p) {
+  __shared__ double scratch[4][kThreads / 32];
+  pdl_trigger();
+  pdl_wait();
+  const int group = threadIdx.x >> 8, c = 4 * (int)cta_rank() + group;
+  const Group g{(int)(threadIdx.x & 255), 1 + group, scratch[group]};
+  if (c < p.nctas) norm_share<false>(p, c, g);
+  cluster_sync();
+  const int n_rec = p.ntens ? p.nctas + p.ntens - 1 : 0;
+  if (!p.scale) {
+    if (c != 0) return;
+    if (p.each)
+      norms_of_each(p.kind, p.rec, p.each, p.ntens, p.n_empty, p.nwin, p.nctas, g.tid,
+                    [&](int k) { return TensPlace{k < p.ntens ? p.t[k].win_begin : p.nwin, p.index[k]}; });
+    const double v = join_records(p.kind, p.rec, n_rec, g);
+    if (g.tid == 0) write_total(p.total, p.status, norm_of(p.kind, v), p.max_norm);
+    return;
   }
+  if (c >= p.nctas) return;
+  const float norm = norm_of(p.kind, join_records(p.kind, p.rec, n_rec, g));
+  if (c == 0 && g.tid == 0) write_total(p.total, p.status, norm, p.max_norm);
+  scale_share(p, c, factor_of(norm, p.max_norm), g.tid);
 }
 
 }  // namespace
@@ -402,6 +453,23 @@ static cudaError_t with_capacity(int n, F &&launch) {
   if (n <= kFewTens) return launch(std::integral_constant<int, kFewTens>());
   if (n <= kSomeTens) return launch(std::integral_constant<int, kSomeTens>());
   return launch(std::integral_constant<int, kMaxTens>());
+}
+
+cudaError_t launch_tens_small(const TensSmallParams &p, cudaStream_t s) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(kSmallCtas);
+  cfg.blockDim = dim3(kSmallThreads);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = kSmallCtas;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, tens_small_kernel, p);
 }
 
 cudaError_t launch_tens_norm(const TensParams &p, cudaStream_t s) {

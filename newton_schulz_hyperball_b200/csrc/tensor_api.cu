@@ -127,6 +127,41 @@ nshb_status fill_launch(const nshb_tensor *src, const nshb_tensor *dst, int32_t 
   return NSHB_OK;
 }
 
+// The whole call in one launch where the list is short.  Otherwise *done stays false and nothing is queued.
+nshb_status run_small(const nshb_tensor *src, const nshb_tensor *dst, int32_t n, int32_t kind, float max_norm, float *total,
+                      float *each, bool scale, const TensWorkspace &w, cudaStream_t st, bool *done) {
+  *done = false;
+  if (n > kSmallWindows) return NSHB_OK;
+  int64_t bytes = 0;   // windows are of 16 KB at most: a quick bound before the records are made
+  for (int32_t i = 0; i < n; ++i) {
+    bytes += src[i].rows * src[i].cols * (src[i].dtype == NSHB_F32 ? 4 : 2);
+    if (bytes > (int64_t)kSmallWindows * kWinBytes) return NSHB_OK;
+  }
+  TensSmallParams p;
+  static_cast<TensSmallHead &>(p) = TensSmallHead{};
+  int64_t win = 0;
+  for (int32_t i = 0; i < n; ++i) {
+    if (src[i].rows == 0 || src[i].cols == 0) continue;
+    const nshb_tensor *d = scale ? (dst ? &dst[i] : &src[i]) : nullptr;
+    if (!fill(src[i], d, win, p.t[p.ntens]) || win > (scale ? kSmallClipWindows : kSmallWindows)) return NSHB_OK;
+    p.index[p.ntens++] = i;
+  }
+  for (int32_t i = 0; i < n; ++i)
+    if (src[i].rows == 0 || src[i].cols == 0) p.index[p.ntens + p.n_empty++] = i;
+  p.nwin = (int32_t)win;
+  p.nctas = std::min(p.nwin, 4 * kSmallCtas);
+  p.rec = w.rec;
+  p.total = total;
+  p.status = w.status;
+  p.max_norm = max_norm;
+  p.kind = kind;
+  p.each = each;
+  p.scale = scale;
+  *done = true;
+  NSHB_RUN(NSHB_PROF_GRAD, launch_tens_small(p, st));
+  return NSHB_OK;
+}
+
 // Norm launches over the whole list.  `one` (optional): where the list fits one launch, its records are left
 // for the caller, who forms the norm itself (no finalize kernel).
 nshb_status run_norm(const nshb_tensor *g, int32_t n, int32_t kind, float max_norm, float *total, float *each,
@@ -260,7 +295,11 @@ nshb_status nshb_grad_norm(const nshb_tensor *g, int32_t n, int32_t kind, float 
   if ((uintptr_t)each % sizeof(float)) return NSHB_ERR_SHAPE;
   e = check_tens_ws(ws, ws_bytes, n);
   if (e != NSHB_OK) return e;
-  return run_norm(g, n, kind, max_norm, total, each, tens_workspace(ws, n), (cudaStream_t)stream, nullptr);
+  const TensWorkspace w = tens_workspace(ws, n);
+  bool done;
+  e = run_small(g, nullptr, n, kind, max_norm, total, each, /*scale=*/false, w, (cudaStream_t)stream, &done);
+  if (e != NSHB_OK || done) return e;
+  return run_norm(g, n, kind, max_norm, total, each, w, (cudaStream_t)stream, nullptr);
 }
 
 nshb_status nshb_clip_grads(const nshb_tensor *src, const nshb_tensor *dst, int32_t n, int32_t kind, float max_norm,
@@ -273,6 +312,9 @@ nshb_status nshb_clip_grads(const nshb_tensor *src, const nshb_tensor *dst, int3
   if (e != NSHB_OK) return e;
   const TensWorkspace w = tens_workspace(ws, n);
   cudaStream_t st = (cudaStream_t)stream;
+  bool done;
+  e = run_small(src, dst, n, kind, max_norm, total, nullptr, /*scale=*/has_elements(src, n), w, st, &done);
+  if (e != NSHB_OK || done) return e;
   if (!has_elements(src, n)) return run_norm(src, n, kind, max_norm, total, nullptr, w, st, nullptr);
   int32_t n_rec = -1;
   e = run_norm(src, n, kind, max_norm, total, nullptr, w, st, &n_rec);

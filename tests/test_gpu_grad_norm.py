@@ -60,6 +60,9 @@ SETS = {
     "one short vector": [(7,)],
     "one window": [(4096,)],
     "one window and one": [(8193,)],
+    "a window for each group": [(4096,)] * 32,
+    "one more": [(4096,)] * 33,
+    "short ones and empty ones": [(0,), (100,), (0, 3), (9000,), (50, 60)],
     "vectors": [(128,), (2048,), (1,), (33,), (4097,)] * 5,
     "matrices": [(64, 64), (5, 7), (768, 768), (1, 9), (300, 700), (130, 1)],
     "a large one": [(2048, 2049), (3,)],
@@ -150,10 +153,10 @@ def test_not_finite(kind, dtype, bad):
 
 @pytest.mark.parametrize("src_dtype", [torch.bfloat16, torch.float32])
 @pytest.mark.parametrize("dst_dtype", [torch.bfloat16, torch.float32])
-@pytest.mark.parametrize("count", [1, 800])
+@pytest.mark.parametrize("count", [0, 1, 800])
 @pytest.mark.parametrize("offset", [0, 1, 5, 8])
 def test_clip_into(src_dtype, dst_dtype, count, offset):
-    shapes = [(33, 65), (1, 5000), (700, 301)] + [(1, 3)] * count
+    shapes = [(33, 65), (1, 5000), (700, 301) if count else (70, 31)] + [(1, 3)] * count
     src = make(shapes, src_dtype, seed=count)
     lds = [c + (9 if i == 2 else 0) for i, (_, c) in enumerate(shapes)]
     size = sum(r * ld for (r, _), ld in zip(shapes, lds))
