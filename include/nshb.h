@@ -310,8 +310,8 @@ nshb_status nshb_grad_norm(const nshb_tensor *g, int32_t n, int32_t kind, float 
 
 /* nshb_grad_norm, then every element multiplied by total[1] in fp32 and rounded once into
  * dst[i] (same rows and cols as src[i], any ld and dtype; dst == NULL: in place).  dst[i].data is
- * either src[i].data (with the same ld and dtype) or does not overlap any source.  Elements between cols and
- * ld are not written.  In place and with a factor of 1, nothing is written. */
+ * either src[i].data (with the same ld and dtype) or does not overlap any source; no two destinations (in place:
+ * no two tensors) overlap.  Elements between cols and ld are not written.  In place and with a factor of 1, nothing is written. */
 nshb_status nshb_clip_grads(const nshb_tensor *src, const nshb_tensor *dst, int32_t n, int32_t kind, float max_norm,
                             float *total, void *ws, size_t ws_bytes, nshb_stream stream);
 
@@ -358,14 +358,15 @@ nshb_status nshb_fp4_size(int64_t rows, int64_t cols, int32_t format, size_t *co
 nshb_status nshb_fp4_quantize(const nshb_tensor *X, const nshb_fp4 *Q, int32_t n, int32_t transpose, void *ws,
                               size_t ws_bytes, nshb_stream stream);
 
-/* X[i] = the values of Q[i] (same rows and cols), rounded once to X[i]'s dtype. */
+/* X[i] = the values of Q[i] (same rows and cols), rounded once to X[i]'s dtype.  Neither here nor in
+ * nshb_fp4_quantize may destinations overlap one another or a source. */
 nshb_status nshb_fp4_dequantize(const nshb_fp4 *Q, const nshb_tensor *X, int32_t n, nshb_stream stream);
 
 /* D[i] = A[i] B[i]^T (rows of A x rows of B, bf16 or fp32, any ld), or with B == NULL the Gram matrix
  * A[i] A[i]^T (both triangles): products of 4-bit matrices of one format and equal cols on the tensor
  * cores, fp32 accumulation, multiplied by both global scales and rounded once.  cols == 0 gives
- * zeros.  A NaN scale makes the rows (columns) of D that use it NaN.  D must not overlap the
- * operands.  The tensor cores read the operands in place.  Any sizes from one row (a single token) on;
+ * zeros.  A NaN scale makes the rows (columns) of D that use it NaN.  No D overlaps an
+ * operand or another D.  The tensor cores read the operands in place.  Any sizes from one row (a single token) on;
  * the number of CTAs that share a sum, and so its order, depends on the sizes and on nothing else.
  * ws: nshb_tensor_workspace_size(D, n) bytes; its status word is cleared first and gets
  * NSHB_DEV_TIMEOUT if a bounded wait ran out. */

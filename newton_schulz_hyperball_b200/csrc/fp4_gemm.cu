@@ -175,15 +175,17 @@ __device__ __forceinline__ void store_block(const Fp4Prob &q, uint8_t *stage, in
 __device__ __forceinline__ void store_mirror(const Fp4Prob &q, int64_t row, int64_t c, const float (&v)[32]) {
   const int64_t row0 = row - (threadIdx.x & 31);
   if (c >= row0 + 31 || row >= q.np) return;
-  const bool f32 = q.flags & kFp4DF32, below = c + 31 < row0;   // else the block crosses the diagonal
+  const bool whole = c + 31 < row0 && c + 32 <= q.nq;   // else the block crosses the diagonal or D's end
+  if (q.flags & kFp4DF32) {
+    float *d = static_cast<float *>(q.d) + c * q.ld + row;
 #pragma unroll
-  for (int e = 0; e < 32; ++e) {
-    if (c + e >= q.nq) break;
-    const int64_t at = (c + e) * q.ld + row;
-    if (below || c + e < row) {
-      if (f32) static_cast<float *>(q.d)[at] = v[e];
-      else static_cast<__nv_bfloat16 *>(q.d)[at] = __float2bfloat16_rn(v[e]);
-    }
+    for (int e = 0; e < 32; ++e, d += q.ld)
+      if (whole || (c + e < row && c + e < q.nq)) *d = v[e];
+  } else {
+    __nv_bfloat16 *d = static_cast<__nv_bfloat16 *>(q.d) + c * q.ld + row;
+#pragma unroll
+    for (int e = 0; e < 32; ++e, d += q.ld)
+      if (whole || (c + e < row && c + e < q.nq)) *d = __float2bfloat16_rn(v[e]);
   }
 }
 

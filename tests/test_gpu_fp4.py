@@ -91,11 +91,37 @@ def test_borders_between_codes(fmt, dtype, transpose):
 
 
 @pytest.mark.parametrize("fmt", FORMATS)
-@pytest.mark.parametrize("scale", [1e-45, 1e-39, 1e-37, 1e-30, 1.0, 1e30, 3e38])
-def test_the_whole_range_of_fp32(fmt, scale):
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("transpose", [False, True])
+@pytest.mark.parametrize("scale", [1e-45, 1e-40, 1e-39, 1e-37, 1e-30, 1.0, 1e30, 3e38])
+def test_the_whole_range_of_the_exponent(fmt, dtype, transpose, scale):
     x = matrix(70, 100, torch.float32, seed=3, spread=0.5).double()
-    x = (x / x.abs().max() * scale).float().to(DEV)
-    check(x, quantize([x], fmt)[0], fmt)
+    x = (x / x.abs().max() * scale).to(dtype).to(DEV)
+    check(x, quantize([x], fmt, transpose)[0], fmt, transpose)
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("transpose", [False, True])
+def test_more_tiles_than_the_gpu_takes_at_once(fmt, transpose):
+    xs = [matrix(r, c, torch.bfloat16, seed=r).to(DEV) for r, c in ((1500, 3000), (130, 1290), (2000, 2600))]
+    for x, q in zip(xs, quantize(xs, fmt, transpose)):
+        check(x, q, fmt, transpose)
+
+
+@pytest.mark.parametrize("transpose", [False, True])
+def test_dtypes_and_formats_in_one_list(transpose):
+    kinds = [(d, f) for d in DTYPES for f in FORMATS] * 2
+    xs = [matrix(40 + 7 * i, 90 - 5 * i, d, seed=i).to(DEV) for i, (d, _) in enumerate(kinds)]
+    qs = [nshb.fp4_empty(*(x.shape[::-1] if transpose else x.shape), f, DEV) for x, (_, f) in zip(xs, kinds)]
+    h = nshb.tensors(xs)
+    nshb.fp4_quantize(h, nshb.fp4_matrices(qs), nshb.tensor_workspace(h), transpose=transpose)
+    outs = [torch.empty(q.rows, q.cols, dtype=d, device=DEV) for q, (d, _) in zip(qs, kinds[::-1])]
+    nshb.fp4_dequantize(nshb.fp4_matrices(qs), nshb.tensors(outs))
+    for x, q, o, (_, f) in zip(xs, qs, outs, kinds):
+        check(x, q, f, transpose)
+        one = torch.empty_like(o)
+        nshb.fp4_dequantize(nshb.fp4_matrices([q]), nshb.tensors([one]))
+        assert torch.equal(o, one)
 
 
 @pytest.mark.parametrize("fmt", FORMATS)
