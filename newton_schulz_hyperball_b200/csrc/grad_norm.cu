@@ -69,7 +69,7 @@ __device__ __forceinline__ float factor_of(float norm, float max_norm) {
 
 __device__ __forceinline__ double square(float x) { return (double)x * (double)x; }
 
-// Eight squares are summed in fp32 (three roundings deep) and the sum is carried in fp64; where the
+// Eight squares are summed in fp32 (four roundings deep) and the sum is carried in fp64; where the
 // fp32 sum left the range in which no square can have been lost or have overflowed, the
 // eight are summed again in fp64.
 struct SumSquares {
@@ -85,7 +85,6 @@ struct SumSquares {
       for (int e = 0; e < 8; ++e) acc += square(x[e]);
     }
   }
-  __device__ __forceinline__ void add1(float x) { acc += square(x); }
   __device__ __forceinline__ double value() const { return acc; }
 };
 template <bool FINITE>
@@ -161,6 +160,30 @@ __device__ __forceinline__ const char *run_ptr(const TensRec &q, const Place &l)
   return static_cast<const char *>(q.src) + ((int64_t)l.row * q.sld + l.at) * (F32 ? 4 : 2);
 }
 
+// A thread's share of a partial window, zeros outside the run: every load under way before the first is used.
+template <bool F32>
+__device__ __forceinline__ void load_partial(const TensRec &q, const Place &l, float (&x)[Share<F32>::E]) {
+  const char *row = static_cast<const char *>(q.src) + (int64_t)l.row * q.sld * (F32 ? 4 : 2);
+#pragma unroll
+  for (int e = 0; e < Share<F32>::E; ++e)
+    x[e] = l.at + e >= 0 && l.at + e < q.cols ? load1<F32>(row, l.at + e) : 0.f;
+}
+
+// Walks the elements of a window of short rows, kThreads apart, without a division an element.
+struct ShortRows {
+  int r, j, dr, dj, cols;
+  __device__ __forceinline__ ShortRows(int tid, int cols_)
+      : r(tid / cols_), j(tid - tid / cols_ * cols_), dr(kThreads / cols_), dj(kThreads - kThreads / cols_ * cols_), cols(cols_) {}
+  __device__ __forceinline__ void next() {
+    r += dr;
+    j += dj;
+    if (j >= cols) {
+      j -= cols;
+      ++r;
+    }
+  }
+};
+
 template <class V, bool F32, bool TWO>
 __device__ __forceinline__ double norm_windows(const TensRec &q, int w, int wend, int tid) {
   V v;
@@ -180,10 +203,16 @@ __device__ __forceinline__ double norm_windows(const TensRec &q, int w, int wend
         s.load(run_ptr<F32>(q, l));
         add(s);
       } else {
-        const char *row = static_cast<const char *>(q.src) + (int64_t)l.row * q.sld * (F32 ? 4 : 2);
-        const int64_t lo = l.at > 0 ? l.at : 0;
-        const int64_t hi = l.at + Share<F32>::E < q.cols ? l.at + Share<F32>::E : q.cols;
-        for (int64_t i = lo; i < hi; ++i) v.add1(load1<F32>(row, i));
+        if (l.at + Share<F32>::E <= 0 || l.at >= q.cols) return;
+        float x[Share<F32>::E];
+        load_partial<F32>(q, l, x);
+#pragma unroll
+        for (int g = 0; g < Share<F32>::E / 8; ++g) {
+          float y[8];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) y[e] = x[8 * g + e];
+          v.add8(y);
+        }
       }
     };
     // two windows at a time: 128 bytes of each thread in flight
@@ -205,9 +234,13 @@ __device__ __forceinline__ double norm_windows(const TensRec &q, int w, int wend
     for (; w < wend; ++w) {
       const int r0 = w * q.per_row, cols = (int)q.cols;
       const int nr = q.rows - r0 < q.per_row ? q.rows - r0 : q.per_row;
-      for (int i = tid; i < nr * cols; i += kThreads) {
-        const int r = i / cols;
-        v.add1(load1<F32>(q.src, (int64_t)(r0 + r) * q.sld + (i - r * cols)));
+      ShortRows at(tid, cols);
+      while (at.r < nr) {
+        float x[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e, at.next())
+          x[e] = at.r < nr ? load1<F32>(q.src, (int64_t)(r0 + at.r) * q.sld + at.j) : 0.f;
+        v.add8(x);
       }
     }
   }
@@ -363,18 +396,28 @@ __device__ __forceinline__ void scale_windows(const TensRec &q, int w, int wend,
         for (int e = 0; e < E; ++e) y[e] = f * s.get(e);
         store_share<DF32, E>(drow + l.at * (DF32 ? 4 : 2), y);
       } else {
-        const char *row = static_cast<const char *>(q.src) + (int64_t)l.row * q.sld * (F32 ? 4 : 2);
-        const int64_t lo = l.at > 0 ? l.at : 0, hi = l.at + E < q.cols ? l.at + E : q.cols;
-        for (int64_t i = lo; i < hi; ++i) store1<DF32>(drow, i, f * load1<F32>(row, i));
+        if (l.at + E <= 0 || l.at >= q.cols) continue;
+        float x[E];
+        load_partial<F32>(q, l, x);
+#pragma unroll
+        for (int e = 0; e < E; ++e)
+          if (l.at + e >= 0 && l.at + e < q.cols) store1<DF32>(drow, l.at + e, f * x[e]);
       }
     }
   } else {
     for (int u = wend - 1; u >= w; --u) {
       const int r0 = u * q.per_row, cols = (int)q.cols;
       const int nr = q.rows - r0 < q.per_row ? q.rows - r0 : q.per_row;
-      for (int i = tid; i < nr * cols; i += kThreads) {
-        const int r = i / cols, j = i - r * cols;
-        store1<DF32>(q.dst, (int64_t)(r0 + r) * q.dld + j, f * load1<F32>(q.src, (int64_t)(r0 + r) * q.sld + j));
+      ShortRows at(tid, cols);
+      while (at.r < nr) {
+        float x[8];
+        ShortRows to = at;
+#pragma unroll
+        for (int e = 0; e < 8; ++e, at.next())
+          x[e] = at.r < nr ? load1<F32>(q.src, (int64_t)(r0 + at.r) * q.sld + at.j) : 0.f;
+#pragma unroll
+        for (int e = 0; e < 8; ++e, to.next())
+          if (to.r < nr) store1<DF32>(q.dst, (int64_t)(r0 + to.r) * q.dld + to.j, f * x[e]);
       }
     }
   }
