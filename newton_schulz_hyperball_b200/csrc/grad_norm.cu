@@ -289,7 +289,7 @@ __device__ __forceinline__ void norm_share(const P &p, int c, const Group &g) {
 }
 
 template <int N>
-__global__ void __launch_bounds__(kThreads, kNormCtasPerSm) tens_norm_kernel(const __grid_constant__ TensBlock<N> p) {
+__global__ void __launch_bounds__(kThreads, kTensCtasPerSm) tens_norm_kernel(const __grid_constant__ TensBlock<N> p) {
   __shared__ double scratch[kThreads / 32];
   pdl_trigger();
   pdl_wait();
@@ -380,30 +380,47 @@ __device__ __forceinline__ void store_share(char *d, const float (&y)[E]) {
   }
 }
 
-template <bool F32, bool DF32>
+template <bool F32, bool DF32, bool TWO>
 __device__ __forceinline__ void scale_windows(const TensRec &q, int w, int wend, float f, int tid) {
   constexpr int E = Share<F32>::E;
   // backwards: the windows that the norm read last are still in the L2 cache
   if (q.flags & kTensRun) {
-    for (int u = wend - 1; u >= w; --u) {
-      const Place l = place<F32>(q, u, tid);
-      char *drow = static_cast<char *>(q.dst) + (int64_t)l.row * q.dld * (DF32 ? 4 : 2);
+    auto out = [&](const Place &l, const Share<F32> &s) {
+      float y[E];
+#pragma unroll
+      for (int e = 0; e < E; ++e) y[e] = f * s.get(e);
+      store_share<DF32, E>(static_cast<char *>(q.dst) + ((int64_t)l.row * q.dld + l.at) * (DF32 ? 4 : 2), y);
+    };
+    auto one = [&](const Place &l) {
       if (l.whole) {
         Share<F32> s;
         s.load(run_ptr<F32>(q, l));
-        float y[E];
-#pragma unroll
-        for (int e = 0; e < E; ++e) y[e] = f * s.get(e);
-        store_share<DF32, E>(drow + l.at * (DF32 ? 4 : 2), y);
+        out(l, s);
       } else {
-        if (l.at + E <= 0 || l.at >= q.cols) continue;
+        if (l.at + E <= 0 || l.at >= q.cols) return;
         float x[E];
         load_partial<F32>(q, l, x);
+        char *drow = static_cast<char *>(q.dst) + (int64_t)l.row * q.dld * (DF32 ? 4 : 2);
 #pragma unroll
         for (int e = 0; e < E; ++e)
           if (l.at + e >= 0 && l.at + e < q.cols) store1<DF32>(drow, l.at + e, f * x[e]);
       }
+    };
+    int u = wend - 1;
+    for (; TWO && u > w; u -= 2) {
+      const Place l0 = place<F32>(q, u, tid), l1 = place<F32>(q, u - 1, tid);
+      if (l0.whole && l1.whole) {
+        Share<F32> s0, s1;
+        s0.load(run_ptr<F32>(q, l0));
+        s1.load(run_ptr<F32>(q, l1));
+        out(l0, s0);
+        out(l1, s1);
+      } else {
+        one(l0);
+        one(l1);
+      }
     }
+    for (; u >= w; --u) one(place<F32>(q, u, tid));
   } else {
     for (int u = wend - 1; u >= w; --u) {
       const int r0 = u * q.per_row, cols = (int)q.cols;
@@ -423,7 +440,7 @@ __device__ __forceinline__ void scale_windows(const TensRec &q, int w, int wend,
   }
 }
 
-template <class P>
+template <bool TWO, class P>
 __device__ __forceinline__ void scale_share(const P &p, int c, float f, int tid) {
   const int w0 = (int)((int64_t)c * p.nwin / p.nctas), w1 = (int)((int64_t)(c + 1) * p.nwin / p.nctas);
   for (int t = find_tensor(p, w1 - 1), w = w1; w > w0; --t) {
@@ -433,10 +450,10 @@ __device__ __forceinline__ void scale_share(const P &p, int c, float f, int tid)
     const bool still = f == 1.f && q.src == q.dst;   // in place: the values stay as they are
     if (!still) {
       switch (q.flags & (kTensF32 | kTensDstF32)) {
-        case 0: scale_windows<false, false>(q, a, b, f, tid); break;
-        case kTensF32: scale_windows<true, false>(q, a, b, f, tid); break;
-        case kTensDstF32: scale_windows<false, true>(q, a, b, f, tid); break;
-        default: scale_windows<true, true>(q, a, b, f, tid); break;
+        case 0: scale_windows<false, false, TWO>(q, a, b, f, tid); break;
+        case kTensF32: scale_windows<true, false, TWO>(q, a, b, f, tid); break;
+        case kTensDstF32: scale_windows<false, true, TWO>(q, a, b, f, tid); break;
+        default: scale_windows<true, true, TWO>(q, a, b, f, tid); break;
       }
     }
     w = wb;
@@ -446,7 +463,7 @@ __device__ __forceinline__ void scale_share(const P &p, int c, float f, int tid)
 // The factor is read, or formed from the norm's records by every CTA for itself (a few KB from L2,
 // no launch between the norm and the scaling).
 template <int N>
-__global__ void __launch_bounds__(kThreads, kScaleCtasPerSm) tens_scale_kernel(const __grid_constant__ TensBlock<N> p) {
+__global__ void __launch_bounds__(kThreads, kTensCtasPerSm) tens_scale_kernel(const __grid_constant__ TensBlock<N> p) {
   __shared__ double scratch[kThreads / 32];
   pdl_trigger();
   pdl_wait();
@@ -458,7 +475,7 @@ __global__ void __launch_bounds__(kThreads, kScaleCtasPerSm) tens_scale_kernel(c
   } else {
     f = *p.factor;
   }
-  scale_share(p, blockIdx.x, f, threadIdx.x);
+  scale_share<true>(p, blockIdx.x, f, threadIdx.x);
 }
 
 // All of a call on a short list: one cluster of kSmallCtas CTAs, four groups each.  The records cross between
@@ -485,7 +502,7 @@ __global__ void __launch_bounds__(kSmallThreads, 1) tens_small_kernel(const __gr
   if (c >= p.nctas) return;
   const float norm = norm_of(p.kind, join_records(p.kind, p.rec, n_rec, g));
   if (c == 0 && g.tid == 0) write_total(p.total, p.status, norm, p.max_norm);
-  scale_share(p, c, factor_of(norm, p.max_norm), g.tid);
+  scale_share<false>(p, c, factor_of(norm, p.max_norm), g.tid);
 }
 
 }  // namespace

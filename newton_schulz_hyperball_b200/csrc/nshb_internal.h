@@ -355,8 +355,9 @@ struct DiagParams {
 constexpr int kWinBytes = 16384;
 constexpr int kMaxTens = 512;
 constexpr int kLongRow = 256;
-constexpr int kNormCtasPerSm = 3;    // 128 bytes of each thread in flight, 85 registers
-constexpr int kScaleCtasPerSm = 4;   // 64 bytes, 64 registers
+// 128 bytes of each thread in flight, 85 registers.  The norm and the scaling split the line alike, so that a CTA's
+// scaling starts with what its norm read last.
+constexpr int kTensCtasPerSm = 3;
 constexpr int kTensF32 = 1;      // source is fp32 (else bf16)
 constexpr int kTensDstF32 = 2;   // destination is fp32 (else bf16)
 constexpr int kTensRun = 4;      // windows of runs (else several short rows to a window)

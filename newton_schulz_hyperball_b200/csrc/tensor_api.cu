@@ -53,7 +53,7 @@ nshb_status check_tens_ws(void *ws, size_t bytes, int32_t n) {
   return NSHB_OK;
 }
 
-int tens_ctas(int nwin, int per_sm) { return std::min(nwin, std::min(per_sm * device_sms(), kMaxTensCtas)); }
+int tens_ctas(int nwin) { return std::min(nwin, std::min(kTensCtasPerSm * device_sms(), kMaxTensCtas)); }
 
 namespace {
 
@@ -116,7 +116,7 @@ nshb_status fill_launch(const nshb_tensor *src, const nshb_tensor *dst, int32_t 
     ++p.ntens;
   }
   p.nwin = (int32_t)win;
-  p.nctas = tens_ctas(p.nwin, dst ? kScaleCtasPerSm : kNormCtasPerSm);
+  p.nctas = tens_ctas(p.nwin);
   if (fin) {
     for (int32_t k = 0; k < n_empty; ++k) fin->at[p.ntens + k] = {p.nwin, empty[k]};
     fin->ntens = p.ntens;

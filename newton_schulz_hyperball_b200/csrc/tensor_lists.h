@@ -32,7 +32,7 @@ TensWorkspace tens_workspace(void *ws, int32_t n);
 nshb_status check_tens_ws(void *ws, size_t bytes, int32_t n);
 nshb_status check_tensor(const nshb_tensor &t);
 nshb_status check_tensors(const nshb_tensor *t, int32_t n);
-int tens_ctas(int nwin, int per_sm);
+int tens_ctas(int nwin);
 // The largest finite magnitude of each of up to kMaxTens tensors with elements, left as records: tensor k's
 // are w.rec[rec_begin[k]] .. [+ n_rec[k]), each the bits of a magnitude as a double.
 nshb_status run_largest(const nshb_tensor *t, int32_t n, const TensWorkspace &w, cudaStream_t st, int32_t *rec_begin,
