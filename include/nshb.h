@@ -311,7 +311,8 @@ nshb_status nshb_grad_norm(const nshb_tensor *g, int32_t n, int32_t kind, float 
 /* nshb_grad_norm, then every element multiplied by total[1] in fp32 and rounded once into
  * dst[i] (same rows and cols as src[i], any ld and dtype; dst == NULL: in place).  dst[i].data is
  * either src[i].data (with the same ld and dtype) or does not overlap any source; no two destinations (in place:
- * no two tensors) overlap.  Elements between cols and ld are not written.  In place and with a factor of 1, nothing is written. */
+ * no two tensors) overlap.  Elements between cols and ld are not written.  In place and with a factor of
+ * 1, nothing is written. */
 nshb_status nshb_clip_grads(const nshb_tensor *src, const nshb_tensor *dst, int32_t n, int32_t kind, float max_norm,
                             float *total, void *ws, size_t ws_bytes, nshb_stream stream);
 

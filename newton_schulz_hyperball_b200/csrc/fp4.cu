@@ -6,11 +6,15 @@
 // Bound by HBM: 2 (or 4) bytes read and 0.53 (0.56) written per element.  A CTA takes a tile of 128 rows x 128
 // columns, so that every 128-byte line of the source, every 64-byte piece of a row of codes and
 // every 512-byte tile of scales is moved whole.  A lane takes 8 columns, 16 lanes a row: each load and store
-// instruction of a warp covers two whole pieces of rows (32 columns a lane, 64 bytes apart, took
-// twice as long for the values).  The CTAs are persistent and load ahead: a batch of rows of the same or the next
-// tile is under way while one is processed.  For the transpose the tile goes through shared memory as 32-bit words, whose place is permuted by
+// instruction of a warp covers two whole pieces of rows.  The CTAs are persistent and load ahead: a batch
+// of rows of the same or the next tile is under way while one is processed.  Four bf16 6144 x 2048
+// matrices: to MXFP4 in 21.4 us (127 MB, 5.9 TB/s; instruction issue 0.66 a clock is the next bound: 28.9 us
+// before whole tiles lost their bounds checks and bf16 its widening), their values in 23.3 us.
+//
+// For the transpose the tile goes through shared memory as 32-bit words, whose place is permuted by
 // the 32-row group (word ^ 8 group), so that the four groups of eight columns that a warp reads
-// fall into different banks.
+// fall into different banks.  8192 x 2048 bf16 to NVFP4: 20.6 us, 8 of them the pass for the largest
+// magnitude, which the matrix's scale needs before the first code.
 #include <cuda_runtime.h>
 
 #include <type_traits>

@@ -5,12 +5,14 @@
 // The codes go from memory to the tensor core as they are stored: one 128-byte box holds 256
 // columns of a row.  The scales of a step (512-byte tiles, see nshb_fp4) are loaded next to the
 // codes and copied into tensor memory by tcgen05.cp, which the same thread issues ahead of the MMAs that
-// read them (the two run in order).
+// read them (the two run in order).  The load and MMA warps stay converged and elect a lane to issue: see
+// elect_one.
 //
 // One CTA computes 128 rows of P x BN rows of Q.  Few rows on one side (single tokens) are bound by
 // the bytes of the other operand: that one takes the 128 lanes, BN is as small as the rows allow,
 // and a cluster of up to 8 CTAs shares the columns of one tile, each summing its part; the parts are joined
-// through distributed shared memory in a fixed order.
+// through distributed shared memory in a fixed order.  One token through 6144 x 2048 NVFP4: 4.5 us (7.1 MB,
+// bound by latency: 8 dependent steps of 0.3 us, of which each CTA's ring holds 5).
 //
 // Enough 256 x 256 tiles to fill the GPU go to CTA pairs (fp4_pair_kernel): a pair reads 64 bytes of
 // codes per clock and SM for the work that single CTAs with 128 x 128 tiles need 128 for.
@@ -460,9 +462,11 @@ __global__ void __launch_bounds__(kThreads, 2) fp4_gemm_kernel(const __grid_cons
   }
 }
 
-// 256 x 256 tiles on CTA pairs, persistent.  What bounds them is shared memory: a step of 256 columns writes 32 KB of
-// codes and 3 or 6 KB of scales into a CTA's and reads them for 513 clocks of MMAs (narrower tiles move more
-// bytes per MMA: 256 x 192 with the scales copied the same way was slower, 8192 x 6144 x 2048 NVFP4).
+// 256 x 256 tiles on CTA pairs, persistent.  8192^3: 177 us MXFP4, 184 us NVFP4 (6.2 and 6.0 PFLOP/s); 8192 x 6144 x 2048
+// NVFP4 to bf16: 48 us (57 with operands and result in DRAM), tensor pipe 50 %; four 2048 x 8192 Gram
+// matrices MXFP4 to fp32: 38 us.  A step of 256 columns is 513 clocks of MMAs and took 600 to 660 in the
+// long sums; what is left is the 870 clocks in which a tile waits for the shared columns below, and the last
+// tile's epilogue (2 us in bf16, 7 us for an fp32 block with its mirror image).
 //
 // Two accumulators of 256 columns and the scales do not fit the 512 columns of tensor memory, so the second
 // accumulator starts 192 columns after the first.  The epilogue drains the 64 shared columns
@@ -470,8 +474,8 @@ __global__ void __launch_bounds__(kThreads, 2) fp4_gemm_kernel(const __grid_cons
 //
 // The MMA warp copies a step's scales into tensor memory ahead of its MMAs: 24 (MX) or 48 columns, a third for this
 // CTA's rows of P, the others for all rows of Q.  Copies and MMAs of one thread run in order and
-// overlap.  The load and MMA warps stay converged and elect a lane to issue (see elect_one; with `lane == 0`
-// code the product above took 83 us, with four more warps for the copies 63 us).
+// overlap.  (8192 x 6144 x 2048 NVFP4 took 83 us with `lane == 0` code instead of an elected lane, 63 us with
+// that and four more warps for the copies, 65 us with them and 256 x 192 tiles.)
 template <bool NV>
 struct PairCfg {
   static constexpr int kBn = kFp4PairBn;

@@ -6,7 +6,10 @@
 // Both are bound by HBM: every element is read once for the norm, and read and written once for
 // the scaling.  All tensors of a launch form one line of 16 KB windows, split evenly over the
 // CTAs, so that a few vectors and a 12-million-element matrix cost their bytes alone; a CTA
-// keeps its sum in registers and reduces it only where its share of a tensor ends.
+// keeps its sum in registers and reduces it only where its share of a tensor ends.  196 bf16 gradients of
+// 1.41 G elements: 396 us (7.1 TB/s of reads); 201 M fp32 elements clipped into bf16: 311 us for the 2.0 GB of
+// three passes (6.5 TB/s; the factor is known only when the last element has been read, and 805 MB do not stay
+// on the chip).
 //
 // Short lists are bound by launches: one cluster does all of a call, each CTA as four groups of 256 threads that
 // take the place of the CTAs of the long form (tens_small_kernel).
