@@ -102,6 +102,14 @@ Shape shape_of(int64_t m, int64_t n, int64_t kt, bool sym, bool pairs) {
   if (kt >= (wide_tile ? 32 : 24) && s.tiles * 8 <= (wide_tile ? sms / 2 : sms)) s.split = 8;
   else if (kt >= 16 && s.tiles * 4 <= sms) s.split = 4;
   else if (kt >= (wide_tile ? 32 : 16) && s.tiles * 2 <= sms) s.split = 2;
+  // Few tiles without a cluster: half as wide ones spread the epilogue over twice the CTAs.
+  if (wide_tile && s.split == 1) {
+    const int64_t narrow = count_tiles(p, q, 128, 64, sym);
+    if (narrow <= sms) {
+      s.bn = 64;
+      s.tiles = narrow;
+    }
+  }
   return s;
 }
 

@@ -258,7 +258,7 @@ __global__ void __launch_bounds__(kThreads, 2) fp4_gemm_kernel(const __grid_cons
         tma_load_2d(sp, &q.pc, kb * 128, pt * 128, full(stage));
         tma_load_2d(sq, &q.qc, kb * 128, qt * BN, full(stage));
         tma_load_3d(ss, &q.ps, 0, kb * C::kSTiles, pt, full(stage));
-        tma_load_3d(ss + C::kPs, &q.qs, 0, kb * C::kSTiles, qt, full(stage));
+        tma_load_3d(ss + C::kPs, &q.qs, 0, kb * C::kSTiles, qt * BN / 128, full(stage));
       }
       __syncwarp();
 #pragma unroll
@@ -275,6 +275,7 @@ __global__ void __launch_bounds__(kThreads, 2) fp4_gemm_kernel(const __grid_cons
       if (last_parity[s] >= 0 && !mbar_wait_warp(full(s), (uint32_t)last_parity[s], limit) && lane == 0)
         set_status(p.status, kTimeoutBit);
   } else if (warp == 1) {
+    const uint32_t qofs = BN < 128 ? (uint32_t)(qt * BN % 128) >> 5 : 0;   // Q's first row within its row tile, in 32s
     int stage = 0;
     uint32_t phase = 0;
     for (int kb = k0; kb < k1; ++kb) {
@@ -295,7 +296,7 @@ __global__ void __launch_bounds__(kThreads, 2) fp4_gemm_kernel(const __grid_cons
           // 64 columns: 32 bytes inside the swizzled rows; MX: half of a scale word, NV: a whole one
           const int j = NV ? k : k >> 1, id = NV ? 0 : 2 * (k & 1);
           tc_mma_fp4<NV>(tmem, smem_desc_sw128(sp + 32 * k, 16, 1024), smem_desc_sw128(sq + 32 * k, 16, 1024),
-                         idesc_fp4(128, BN, NV, id), tmem + C::kPsCol + 4 * j, tmem + C::kQsCol + 4 * j,
+                         idesc_fp4(128, BN, NV, id), tmem + C::kPsCol + 4 * j, tmem + C::kQsCol + 4 * j + qofs,
                          kb != k0 || k != 0);
         }
         tc_commit(empty(stage));
@@ -341,10 +342,10 @@ __global__ void __launch_bounds__(kThreads, 2) fp4_gemm_kernel(const __grid_cons
       // the ring is free: this CTA's MMAs are done
       if (!trans) store_block(q, smem + 2048 * (warp - 2), (int64_t)pt * 128 + 32 * quarter, at, v);
       else store_row<N>(q, (int64_t)pt * 128 + row, at, v, true);
+      if (sym) store_mirror(q, (int64_t)pt * 128 + row, at, v);
     } else {
       store_row<N>(q, (int64_t)pt * 128 + row, at, v, trans);
     }
-    if (sym && pt != qt) store_row<N>(q, (int64_t)pt * 128 + row, (int64_t)qt * BN + c, v, true);
   };
   if (!SPLIT) {
     if (epi) {

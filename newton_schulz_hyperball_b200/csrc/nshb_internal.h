@@ -521,7 +521,7 @@ cudaError_t launch_tens_finalize(const TensFinParams &p, cudaStream_t s);
 cudaError_t launch_tens_scale(const TensParams &p, cudaStream_t s);
 cudaError_t launch_fp4_quantize(const Fp4Params &p, bool transpose, cudaStream_t s);
 cudaError_t launch_fp4_dequantize(const Fp4Params &p, cudaStream_t s);
-// bn: Q rows of a tile: 16, 32, 64 or 128 (below 128 only with one tile along Q) on single CTAs with 128 rows of
+// bn: Q rows of a tile: 16, 32, 64 or 128 (below 64 only with one tile along Q) on single CTAs with 128 rows of
 // P, `split` CTAs of a cluster sharing a tile's columns (1, 2, 4 or 8); or kFp4PairBn on CTA pairs with
 // 256 rows of P (split 1, kt > 0, kFp4DTrans unset).
 constexpr int kFp4PairBn = 256;
