@@ -368,7 +368,8 @@ nshb_status nshb_fp4_dequantize(const nshb_fp4 *Q, const nshb_tensor *X, int32_t
  * cores, fp32 accumulation, multiplied by both global scales and rounded once.  cols == 0 gives
  * zeros.  A NaN scale makes the rows (columns) of D that use it NaN.  No D overlaps an
  * operand or another D.  The tensor cores read the operands in place.  Any sizes from one row (a single token) on;
- * the number of CTAs that share a sum, and so its order, depends on the sizes and on nothing else.
+ * the number of CTAs that share a sum, and so its order, depends on the sizes of the call's matrices and the
+ * GPU's number of SMs alone.
  * ws: nshb_tensor_workspace_size(D, n) bytes; its status word is cleared first and gets
  * NSHB_DEV_TIMEOUT if a bounded wait ran out. */
 nshb_status nshb_fp4_matmul(const nshb_fp4 *A, const nshb_fp4 *B, const nshb_tensor *D, int32_t n, void *ws,

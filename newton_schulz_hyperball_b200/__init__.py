@@ -295,7 +295,7 @@ def newton_muon_step_fp4(mats, Z, p, ws, stream=None):
     _check_rho(p, _n(mats))
     ptr, nbytes = _ws(ws)
     _on("newton_muon_step_fp4", Z, (("W[0]", _first_weight(mats)), ("workspace", ws)), stream,
-        mats, _n(mats), Z, _n(Z), ctypes.byref(p), ptr, nbytes)
+        mats, _n(mats), _arg(Z, nshb_fp4), _n(Z), ctypes.byref(p), ptr, nbytes)
 
 
 def step_scaled(op: int, mats, p, factor, ws, stream=None):
@@ -354,9 +354,14 @@ def tensors(ts):
             raise ValueError(f"tensor {i} must be 2-D with unit column stride, or contiguous")
         arr[i].dtype = _dtype_code(t)
         arr[i].data = t.data_ptr()
-    arr._n = len(ts)
-    arr._keep = (list(ts),)
+    return _handle(arr, ts, dev)
+
+
+def _handle(arr, items, dev):
+    arr._n = len(items)
+    arr._keep = (list(items),)
     arr._device = dev
+    arr._addr = ctypes.addressof(arr)
     return arr
 
 
@@ -364,7 +369,7 @@ def tensor_workspace(t):
     """A device workspace for calls on the tensors `t` (see nshb_tensor_workspace_size)."""
     import torch
     out = ctypes.c_size_t(0)
-    _check(lib().nshb_tensor_workspace_size(t, _n(t), ctypes.byref(out)), "nshb_tensor_workspace_size")
+    _check(lib().nshb_tensor_workspace_size(_arg(t), _n(t), ctypes.byref(out)), "nshb_tensor_workspace_size")
     return torch.empty(out.value, dtype=torch.uint8, device=_device_of(t) or "cuda")
 
 
@@ -380,24 +385,41 @@ def _current_stream(index: int) -> int:
     return raw(index) if raw is not None else torch.cuda.current_stream(index).cuda_stream
 
 
+def _arg(arr, struct=nshb_tensor):
+    """What a call passes for an array of `struct`: its address (the array itself if it was built by hand)."""
+    if arr is None:
+        return None
+    if getattr(arr, "_type_", None) is not struct:
+        raise TypeError(f"an array of {struct.__name__} is expected, not {type(arr).__name__}")
+    return getattr(arr, "_addr", arr)
+
+
 def _on(name, handle, others, stream, *args):
     """Calls the library's `name` with the device of `handle` (a tensors or fp4_matrices array) current, on
     `stream` or that device's current stream; `others` (name, tensor or array) have to be on it."""
     import torch
     fn = getattr(_LIB or lib(), name)
-    dev = _device_of(handle)
+    dev = getattr(handle, "_device", None)
     if dev is None:
         _check(fn(*args, _stream(stream)), name)
         return
     index = dev.index
     for what, t in others:
-        if t is None or isinstance(t, (int, tuple)):
+        if t is None:
             continue
-        d = getattr(t, "_device", None)           # an array; else a tensor
-        d = t.get_device() if d is None and hasattr(t, "get_device") else d and d.index
-        if d is not None and d != index:
+        if isinstance(t, torch.Tensor):
+            d = t.get_device()
+        else:
+            d = getattr(t, "_device", None)
+            if d is None:               # a raw pointer, or an array built by hand
+                continue
+            d = d.index
+        if d != index:
             raise ValueError(f"{what} is on cuda:{d}, the tensors on {dev}")
-    st = _current_stream(index) if stream is None else _stream(stream)
+    if stream is not None:
+        st = _stream(stream)
+    else:
+        st = _current_stream(index)
     if index == torch.cuda.current_device():
         status = fn(*args, st)
     else:
@@ -415,7 +437,7 @@ def grad_norm(g, total, ws, max_norm: float = float("inf"), each=None, kind: int
     _device_arg(each, "each", torch.float32, _n(g))
     ptr, nbytes = _ws(ws)
     _on("nshb_grad_norm", g, (("total", total), ("each", each), ("workspace", ws)), stream,
-        g, _n(g), kind, max_norm, _ptr(total), _ptr(each), ptr, nbytes)
+        _arg(g), _n(g), kind, max_norm, _ptr(total), _ptr(each), ptr, nbytes)
 
 
 def clip_grads(g, max_norm: float, total, ws, dst=None, kind: int = NSHB_NORM_L2, stream=None):
@@ -426,7 +448,7 @@ def clip_grads(g, max_norm: float, total, ws, dst=None, kind: int = NSHB_NORM_L2
     _same_count(g, dst)
     ptr, nbytes = _ws(ws)
     _on("nshb_clip_grads", g, (("total", total), ("dst", dst), ("workspace", ws)), stream,
-        g, dst, _n(g), kind, max_norm, _ptr(total), ptr, nbytes)
+        _arg(g), _arg(dst), _n(g), kind, max_norm, _ptr(total), ptr, nbytes)
 
 
 def scale_grads(g, factor, dst=None, stream=None):
@@ -434,7 +456,7 @@ def scale_grads(g, factor, dst=None, stream=None):
     import torch
     _device_arg(factor, "factor", torch.float32, 1)
     _same_count(g, dst)
-    _on("nshb_scale_grads", g, (("factor", factor), ("dst", dst)), stream, g, dst, _n(g), _ptr(factor))
+    _on("nshb_scale_grads", g, (("factor", factor), ("dst", dst)), stream, _arg(g), _arg(dst), _n(g), _ptr(factor))
 
 
 def _same_count(a, b) -> None:
@@ -489,10 +511,7 @@ def fp4_matrices(qs):
             raise ValueError(f"matrix {i}: every matrix must be on one CUDA device")
         arr[i].rows, arr[i].cols, arr[i].format = q.rows, q.cols, q.format
         arr[i].codes, arr[i].scales, arr[i].global_ = _ptr(q.codes), _ptr(q.scales), _ptr(q.global_scale)
-    arr._n = len(qs)
-    arr._keep = (list(qs),)
-    arr._device = dev
-    return arr
+    return _handle(arr, qs, dev)
 
 
 def fp4_quantize(x, q, ws=None, transpose: bool = False, stream=None):
@@ -502,14 +521,14 @@ def fp4_quantize(x, q, ws=None, transpose: bool = False, stream=None):
         raise ValueError(f"{_n(q)} 4-bit matrices for {_n(x)} tensors")
     ptr, nbytes = (None, 0) if ws is None else _ws(ws)
     _on("nshb_fp4_quantize", x, (("q", q), ("workspace", ws)), stream,
-        x, q, _n(x), 1 if transpose else 0, ptr, nbytes)
+        _arg(x), _arg(q, nshb_fp4), _n(x), 1 if transpose else 0, ptr, nbytes)
 
 
 def fp4_dequantize(q, x, stream=None):
     """The values of the 4-bit matrices `q` into the tensors `x`."""
     if _n(x) != _n(q):
         raise ValueError(f"{_n(x)} tensors for {_n(q)} 4-bit matrices")
-    _on("nshb_fp4_dequantize", q, (("x", x),), stream, q, x, _n(q))
+    _on("nshb_fp4_dequantize", q, (("x", x),), stream, _arg(q, nshb_fp4), _arg(x), _n(q))
 
 
 def fp4_matmul(a, b, d, ws, stream=None):
@@ -518,7 +537,8 @@ def fp4_matmul(a, b, d, ws, stream=None):
     if _n(a) != _n(d) or (b is not None and _n(b) != _n(d)):
         raise ValueError(f"{_n(a)} and {_n(b) if b is not None else _n(a)} operands for {_n(d)} results")
     ptr, nbytes = _ws(ws)
-    _on("nshb_fp4_matmul", d, (("a", a), ("b", b), ("workspace", ws)), stream, a, b, d, _n(d), ptr, nbytes)
+    _on("nshb_fp4_matmul", d, (("a", a), ("b", b), ("workspace", ws)), stream,
+        _arg(a, nshb_fp4), _arg(b, nshb_fp4), _arg(d), _n(d), ptr, nbytes)
 
 
 def device_status(ws, stream=None) -> int:

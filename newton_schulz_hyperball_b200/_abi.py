@@ -120,8 +120,10 @@ class nshb_fp4(ctypes.Structure):
 _P = ctypes.c_void_p
 _MATS = ctypes.POINTER(nshb_matrix)
 _PAR = ctypes.POINTER(nshb_params)
-_TENS = ctypes.POINTER(nshb_tensor)
-_FP4 = ctypes.POINTER(nshb_fp4)
+# Arrays of nshb_tensor and nshb_fp4, as arrays or as the addresses that tensors() and fp4_matrices() keep
+# (converting an array on every call costs as much as a small kernel's launch).
+_TENS = ctypes.c_void_p
+_FP4 = ctypes.c_void_p
 SIGNATURES = {
     "nshb_default_params": (ctypes.c_int32, [_PAR]),
     "nshb_workspace_size": (ctypes.c_int32, [_MATS, ctypes.c_int32, _PAR, ctypes.c_int32,

@@ -219,3 +219,21 @@ def test_newton_step_on_4_bit_inputs_refusals():
     assert call(bad) == nshb.NSHB_ERR_NULL
     m[0].z_index = 1
     assert call(good) == nshb.NSHB_ERR_PARAM
+
+
+def test_an_array_of_another_kind_is_refused():
+    t = fake((128, 64))
+    ws = (WS, 1 << 20)
+    q = (nshb.nshb_fp4 * 1)()
+    m = (nshb.nshb_matrix * 1)()
+    calls = [lambda: nshb.grad_norm(m, TOTAL, ws), lambda: nshb.grad_norm([t], TOTAL, ws),
+             lambda: nshb.clip_grads(q, 1.0, TOTAL, ws), lambda: nshb.clip_grads(t, 1.0, TOTAL, ws, dst=m),
+             lambda: nshb.scale_grads(m, TOTAL), lambda: nshb.fp4_quantize(t, t, ws),
+             lambda: nshb.fp4_dequantize(t, t), lambda: nshb.fp4_matmul(t, q, t, ws),
+             lambda: nshb.fp4_matmul(q, t, t, ws), lambda: nshb.fp4_matmul(q, None, q, ws),
+             lambda: nshb.tensor_workspace(q),
+             lambda: nshb.newton_muon_step_fp4(m, t, nshb.nshb_params(), ws)]
+    for i, call in enumerate(calls):
+        with pytest.raises(TypeError, match="an array of nshb_"):
+            call()
+            pytest.fail(f"call {i} went through")
