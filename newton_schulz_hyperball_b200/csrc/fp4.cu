@@ -13,8 +13,9 @@
 //
 // For the transpose the tile goes through shared memory as 32-bit words, whose place is permuted by
 // the 32-row group (word ^ 8 group), so that the four groups of eight columns that a warp reads
-// fall into different banks.  8192 x 2048 bf16 to NVFP4: 20.6 us, 8 of them the pass for the largest
-// magnitude, which the matrix's scale needs before the first code.
+// fall into different banks.  8192 x 2048 bf16 to NVFP4: 16.6 us, 8 of them the pass for the largest
+// magnitude, which the matrix's scale needs before the first code.  Instruction issue bounds the other pass (16.7
+// an element and 12.5 us before whole tiles lost their bounds checks and bf16 its fp32 quotients).
 #include <cuda_runtime.h>
 
 #include <type_traits>
@@ -107,6 +108,18 @@ __device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
   return r;
 }
 
+__device__ __forceinline__ uint32_t fma_bf16x2(uint32_t a, uint32_t b, uint32_t c) {
+  uint32_t r;
+  asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(c));
+  return r;
+}
+// Within one unit of the last place.
+__device__ __forceinline__ float fast_reciprocal(float x) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+
 // 32 consecutive columns as they were loaded.
 template <bool F32>
 struct Cols32 {
@@ -157,7 +170,7 @@ struct Cols8 {
 
 // The scale byte of a block whose largest magnitude has the bits `top`, and what its elements are
 // multiplied with (MX) or divided by (NV: s, and its reciprocal) to become codes.
-template <bool NV>
+template <bool F32, bool NV>
 __device__ __forceinline__ uint32_t block_scale(uint32_t top, float down, float &s, float &r) {
   const bool bad = top >= 0x7f800000u;
   if (!NV) {
@@ -167,10 +180,18 @@ __device__ __forceinline__ uint32_t block_scale(uint32_t top, float down, float 
     return bad ? 255u : b;
   }
   const float m = (bad ? 0.f : __uint_as_float(top)) * down;
-  const float q6 = __fdiv_rn(m, 6.f);
-  const uint32_t sb = to_e4m3(odd(q6, fmaf(-q6, 6.f, m), m));
+  uint32_t sb;
+  if (F32) {
+    const float q6 = __fdiv_rn(m, 6.f);
+    sb = to_e4m3(odd(q6, fmaf(-q6, 6.f, m), m));
+  } else {
+    // A bf16 m (8 bits) is 6 times the border of two scales (5 bits), or differs from it by 2^-8 of itself.
+    // So a quotient that is at most 2^-19 too large and then cut to 12 bits is on the border exactly
+    // where m / 6 is, and on its side of it elsewhere.
+    sb = to_e4m3(__uint_as_float(__float_as_uint(m * (float)((1. + 0x1p-20) / 6.)) & 0xfffff000u));
+  }
   s = from_e4m3(sb);
-  r = s > 0.f ? __frcp_rn(s) : 0.f;
+  r = s > 0.f ? (F32 ? __frcp_rn(s) : fast_reciprocal(s)) : 0.f;
   return bad ? 0x7fu : sb;
 }
 template <bool NV>
@@ -200,16 +221,19 @@ __device__ __forceinline__ uint32_t codes8(const V &v, int first, uint32_t top, 
       x[2 * e + 1] = bf16hi(y);
     }
   } else if constexpr (!F32) {
-    // A bf16 a (8 bits) is the border of two codes (3 bits) times s (4 bits), or differs from it by 2^-8 of
-    // itself.  So a quotient that is at most 2^-19 too large and then cut to 12 bits is on the
-    // border exactly where a / s is, and on its side of it elsewhere.
+    // A bf16 a (8 bits) is the border of two codes (3 bits) times s (4 bits), or differs from it by 1/254 of
+    // itself or more.  So a / s rounded to bf16 is on a border, which is a bf16 value, exactly where a / s
+    // is, and on its side of it elsewhere; so is a (rh + rl), 1 / s in two bf16 parts, in two roundings
+    // (checked for every a and s).  rl is not negative: -0 stays -0.
     const uint32_t d = __float_as_uint(down), d2 = (d >> 16) | (d & 0xffff0000u);
-    const float up = r * (1.f + 0x1p-20f);
+    const float low = r - __uint_as_float(__float_as_uint(r) & 0xffff0000u);
+    const uint32_t rh = __byte_perm(__float_as_uint(r), 0u, 0x3232), rl = pack_bf16(low, low);
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       const uint32_t a = mul_bf16x2(v.w[first / 2 + e], d2);   // exact: a power of two
-      x[2 * e] = __uint_as_float(__float_as_uint(bf16lo(a) * up) & 0xfffff000u);
-      x[2 * e + 1] = __uint_as_float(__float_as_uint(bf16hi(a) * up) & 0xfffff000u);
+      const uint32_t y = fma_bf16x2(a, rh, mul_bf16x2(a, rl));
+      x[2 * e] = bf16lo(y);
+      x[2 * e + 1] = bf16hi(y);
     }
   } else {
 #pragma unroll
@@ -227,7 +251,7 @@ __device__ __forceinline__ uint32_t quantize32(const Cols32<F32> &v, float down,
   for (int h = 0; h < (NV ? 2 : 1); ++h) {
     const uint32_t top = !NV ? v.template top<0, 32>() : h == 0 ? v.template top<0, 16>() : v.template top<16, 16>();
     float s = 0.f, r;
-    scales |= block_scale<NV>(top, down, s, r) << (8 * h);
+    scales |= block_scale<F32, NV>(top, down, s, r) << (8 * h);
 #pragma unroll
     for (int g = 0; g < (NV ? 2 : 4); ++g) codes[2 * h + g] = codes8<F32, NV>(v, 16 * h + 8 * g, top, down, s, r);
   }
@@ -410,7 +434,7 @@ __global__ void __launch_bounds__(kThreads, 4) fp4_quantize_kernel(const __grid_
         top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
         if (!NV) top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
         float s = 0.f, rc;
-        const uint32_t sb = block_scale<NV>(top, down, s, rc);
+        const uint32_t sb = block_scale<F32, NV>(top, down, s, rc);
         const uint32_t c = codes8<F32, NV>(v[i], 0, top, down, s, rc);
         if (16 * k < rows_left) *reinterpret_cast<uint32_t *>(m.codes + (int64_t)k * m.code_step) = c;
         if ((l & (NV ? 1 : 3)) == 0) scale[256 * (k & 1) + 4 * (k >> 1)] = (uint8_t)sb;
@@ -442,6 +466,16 @@ __global__ void __launch_bounds__(kThreads, F32 ? 2 : 3) fp4_quantize_t_kernel(c
   };
   auto load = [&](const Tile &t, Piece (&v)[kLoads]) {
     const Fp4Item &q = p.item[t.item];
+    if ((q.flags & kFp4Vec) && t.tk * kT + kT <= q.cols && t.tr * kT + kT <= q.rows) {
+      const char *src = static_cast<const char *>(q.x) + ((int64_t)(t.tk * kT + lr) * q.ld + t.tr * kT) * (F32 ? 4 : 2) + 4 * lw;
+      const int64_t step = (kThreads / TPR) * q.ld * (F32 ? 4 : 2);
+#pragma unroll
+      for (int i = 0; i < kLoads; ++i) {
+        const uint4 u = *reinterpret_cast<const uint4 *>(src + i * step);
+        v[i].w[0] = u.x; v[i].w[1] = u.y; v[i].w[2] = u.z; v[i].w[3] = u.w;
+      }
+      return;
+    }
 #pragma unroll
     for (int i = 0; i < kLoads; ++i) {
       const int row = t.tk * kT + lr + i * (kThreads / TPR);

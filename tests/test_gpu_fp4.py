@@ -90,6 +90,28 @@ def test_borders_between_codes(fmt, dtype, transpose):
     check(x, quantize([x], fmt, transpose)[0], fmt, transpose)
 
 
+@pytest.mark.parametrize("transpose", [False, True])
+def test_every_bf16_value_under_every_scale(transpose):
+    """NVFP4 with a matrix scale of 1: all bf16 values from an eighth of each scale to six times it, and each
+    bf16 value as the largest of its block."""
+    mantissas = torch.arange(128, 256, dtype=torch.float64) / 128
+    every = torch.cat([mantissas * 2.0 ** e for e in range(-13, 12)])
+    scales = [(1 + m / 8) * 2.0 ** e for e in range(-6, 9) for m in range(8)][:-1] + [m * 2.0 ** -9 for m in range(1, 8)]
+    blocks = []
+    for s in scales:
+        v = every[(every >= s / 8) & (every <= 6 * s)]
+        v = torch.cat([v, v.new_zeros(-len(v) % 15)]).view(-1, 15) * torch.tensor([1.0, -1.0] * 7 + [1.0], dtype=v.dtype)
+        blocks.append(torch.cat([v.new_full((len(v), 1), 6 * s), v], dim=1))
+    tops = every[every <= 2688]
+    blocks.append(torch.cat([tops[:, None], tops.new_zeros(len(tops), 15)], dim=1))
+    b = torch.cat(blocks)
+    x = torch.cat([b, b.new_zeros(-len(b) % 16, 16)]).view(-1, 256)
+    x[0, 0] = 2688.0
+    assert torch.equal(x, x.bfloat16().double())
+    x = (x.t() if transpose else x).contiguous().to(torch.bfloat16).to(DEV)
+    check(x, quantize([x], nshb.NSHB_NVFP4, transpose)[0], nshb.NSHB_NVFP4, transpose)
+
+
 @pytest.mark.parametrize("fmt", FORMATS)
 @pytest.mark.parametrize("dtype", DTYPES)
 @pytest.mark.parametrize("transpose", [False, True])
