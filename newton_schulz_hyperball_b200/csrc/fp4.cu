@@ -13,7 +13,7 @@
 //
 // For the transpose the tile goes through shared memory as 32-bit words, whose place is permuted by
 // the 32-row group (word ^ 8 group), so that the four groups of eight columns that a warp reads
-// fall into different banks.  8192 x 2048 bf16 to NVFP4: 16.6 us, 8 of them the pass for the largest
+// fall into different banks.  8192 x 2048 bf16 to NVFP4: 15.8 us, 7 of them the pass for the largest
 // magnitude, which the matrix's scale needs before the first code.  Instruction issue bounds the other pass (16.7
 // an element and 12.5 us before whole tiles lost their bounds checks and bf16 its fp32 quotients).
 #include <cuda_runtime.h>
@@ -96,12 +96,6 @@ __device__ __forceinline__ int global_exponent(uint32_t top) {
   return e < -126 ? -126 : e;
 }
 
-// The larger magnitudes of two pairs of bf16 (NaN the largest), one instruction.
-__device__ __forceinline__ uint32_t max_magnitude(uint32_t m, uint32_t w) {
-  uint32_t r;
-  asm("{\n\t.reg .b32 a;\n\tabs.bf16x2 a, %2;\n\tmax.NaN.bf16x2 %0, %1, a;\n\t}" : "=r"(r) : "r"(m), "r"(w));
-  return r;
-}
 __device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
   uint32_t r;
   asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));

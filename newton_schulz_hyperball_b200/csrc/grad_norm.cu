@@ -76,6 +76,7 @@ __device__ __forceinline__ double square(float x) { return (double)x * (double)x
 // fp32 sum left the range in which no square can have been lost or have overflowed, the
 // eight are summed again in fp64.
 struct SumSquares {
+  static constexpr bool kOfPairs = false;
   double acc = 0.0;
   __device__ __forceinline__ void add8(const float (&x)[8]) {
     const float a = fmaf(x[0], x[0], x[1] * x[1]), b = fmaf(x[2], x[2], x[3] * x[3]);
@@ -92,7 +93,18 @@ struct SumSquares {
 };
 template <bool FINITE>
 struct LargestBits {
+  static constexpr bool kOfPairs = true;
   uint32_t top = 0;
+  // Of 32 bf16; false, and nothing done, where one of them is not finite and may not count.
+  __device__ __forceinline__ bool add_pairs(const uint32_t (&w)[16]) {
+    uint32_t m = 0;
+#pragma unroll
+    for (int e = 0; e < 16; ++e) m = max_magnitude(m, w[e]);
+    m = max(m << 16, m & 0xffff0000u);
+    if (FINITE && m >= 0x7f800000u) return false;
+    top = top > m ? top : m;
+    return true;
+  }
   __device__ __forceinline__ void add1(float x) {
     const uint32_t b = __float_as_uint(x) & 0x7fffffffu;
     if (!FINITE || b < 0x7f800000u) top = top > b ? top : b;
@@ -192,6 +204,8 @@ __device__ __forceinline__ double norm_windows(const TensRec &q, int w, int wend
   V v;
   if (q.flags & kTensRun) {
     auto add = [&](const Share<F32> &s) {
+      if constexpr (V::kOfPairs && !F32)
+        if (v.add_pairs(s.w)) return;
 #pragma unroll
       for (int g = 0; g < Share<F32>::E / 8; ++g) {
         float x[8];
