@@ -293,9 +293,12 @@ def newton_muon_step_fp4(mats, Z, p, ws, stream=None):
     """Newton-Muon step with 4-bit layer inputs; Z an fp4_matrices array of z_rows x tokens matrices, `ws`
     from workspace(..., NSHB_OP_NEWTON_MUON, z_rows=[rows of each Z], n_tokens=64)."""
     _check_rho(p, _n(mats))
-    ptr, nbytes = _ws(ws)
-    _on("newton_muon_step_fp4", Z, (("W[0]", _first_weight(mats)), ("workspace", ws)), stream,
-        mats, _n(mats), _arg(Z, nshb_fp4), _n(Z), ctypes.byref(p), ptr, nbytes)
+    at = getattr(Z, "_index", None)
+    w = _first_weight(mats)
+    if w is not None and at is not None and w.get_device() != at:
+        raise ValueError(f"W[0] is on {w.device}, the 4-bit matrices on cuda:{at}")
+    _call("newton_muon_step_fp4", at, stream, mats, _n(mats), _arg(Z, nshb_fp4), _n(Z), ctypes.byref(p),
+          *_workspace(ws, at))
 
 
 def step_scaled(op: int, mats, p, factor, ws, stream=None):
@@ -361,6 +364,7 @@ def _handle(arr, items, dev):
     arr._n = len(items)
     arr._keep = (list(items),)
     arr._device = dev
+    arr._index = dev.index if dev is not None else None
     arr._addr = ctypes.addressof(arr)
     return arr
 
@@ -385,46 +389,48 @@ def _current_stream(index: int) -> int:
     return raw(index) if raw is not None else torch.cuda.current_stream(index).cuda_stream
 
 
-def _arg(arr, struct=nshb_tensor):
-    """What a call passes for an array of `struct`: its address (the array itself if it was built by hand)."""
+def _arg(arr, struct=nshb_tensor, index=None, what: str = ""):
+    """What a call passes for an array of `struct`: its address (the array itself if it was built by hand).
+    With an `index`, an array of tensors has to be on that CUDA device."""
     if arr is None:
         return None
     if getattr(arr, "_type_", None) is not struct:
         raise TypeError(f"an array of {struct.__name__} is expected, not {type(arr).__name__}")
+    if index is not None and getattr(arr, "_index", index) not in (index, None):
+        raise ValueError(f"{what} is on cuda:{arr._index}, the tensors on cuda:{index}")
     return getattr(arr, "_addr", arr)
 
 
-def _on(name, handle, others, stream, *args):
-    """Calls the library's `name` with the device of `handle` (a tensors or fp4_matrices array) current, on
-    `stream` or that device's current stream; `others` (name, tensor or array) have to be on it."""
-    import torch
+def _buffer(t, what: str, index, dtype=None, min_numel: int = 0):
+    """The pointer of a tensor that _device_arg accepts, on CUDA device `index` (None: on any)."""
+    if t is None or isinstance(t, int):
+        return t
+    _device_arg(t, what, dtype, min_numel)
+    if index is not None and t.get_device() != index:
+        raise ValueError(f"{what} is on {t.device}, the tensors on cuda:{index}")
+    return t.data_ptr()
+
+
+def _workspace(ws, index):
+    if isinstance(ws, tuple):
+        return ws
+    return _buffer(ws, "workspace", index), ws.nbytes
+
+
+def _call(name, index, stream, *args):
+    """Calls the library's `name` with CUDA device `index` (None: as it is) current, on `stream` or that
+    device's current stream."""
     fn = getattr(_LIB or lib(), name)
-    dev = getattr(handle, "_device", None)
-    if dev is None:
-        _check(fn(*args, _stream(stream)), name)
-        return
-    index = dev.index
-    for what, t in others:
-        if t is None:
-            continue
-        if isinstance(t, torch.Tensor):
-            d = t.get_device()
-        else:
-            d = getattr(t, "_device", None)
-            if d is None:               # a raw pointer, or an array built by hand
-                continue
-            d = d.index
-        if d != index:
-            raise ValueError(f"{what} is on cuda:{d}, the tensors on {dev}")
-    if stream is not None:
-        st = _stream(stream)
+    if index is None:
+        status = fn(*args, _stream(stream))
     else:
-        st = _current_stream(index)
-    if index == torch.cuda.current_device():
-        status = fn(*args, st)
-    else:
-        with torch.cuda.device(dev):
+        import torch
+        st = _current_stream(index) if stream is None else _stream(stream)
+        if index == torch.cuda.current_device():
             status = fn(*args, st)
+        else:
+            with torch.cuda.device(index):
+                status = fn(*args, st)
     if status:
         _check(status, name)
 
@@ -433,30 +439,28 @@ def grad_norm(g, total, ws, max_norm: float = float("inf"), each=None, kind: int
     """The norm of all elements of the tensors `g` into total[0], and the factor that clips them to
     `max_norm` into total[1] (CUDA float32 of 2 elements); each[i], when given, the norm of tensor i."""
     import torch
-    _device_arg(total, "total", torch.float32, 2)
-    _device_arg(each, "each", torch.float32, _n(g))
-    ptr, nbytes = _ws(ws)
-    _on("nshb_grad_norm", g, (("total", total), ("each", each), ("workspace", ws)), stream,
-        _arg(g), _n(g), kind, max_norm, _ptr(total), _ptr(each), ptr, nbytes)
+    at = getattr(g, "_index", None)
+    _call("nshb_grad_norm", at, stream, _arg(g), _n(g), kind, max_norm, _buffer(total, "total", at, torch.float32, 2),
+          _buffer(each, "each", at, torch.float32, _n(g)), *_workspace(ws, at))
 
 
 def clip_grads(g, max_norm: float, total, ws, dst=None, kind: int = NSHB_NORM_L2, stream=None):
     """Scales the tensors `g` so that their norm is at most `max_norm`, in place or into `dst` (a
     tensors() array of the same sizes, of either dtype); `total` as in grad_norm."""
     import torch
-    _device_arg(total, "total", torch.float32, 2)
     _same_count(g, dst)
-    ptr, nbytes = _ws(ws)
-    _on("nshb_clip_grads", g, (("total", total), ("dst", dst), ("workspace", ws)), stream,
-        _arg(g), _arg(dst), _n(g), kind, max_norm, _ptr(total), ptr, nbytes)
+    at = getattr(g, "_index", None)
+    _call("nshb_clip_grads", at, stream, _arg(g), _arg(dst, nshb_tensor, at, "dst"), _n(g), kind, max_norm,
+          _buffer(total, "total", at, torch.float32, 2), *_workspace(ws, at))
 
 
 def scale_grads(g, factor, dst=None, stream=None):
     """Multiplies the tensors `g` by the one-element CUDA float32 tensor `factor`, in place or into `dst`."""
     import torch
-    _device_arg(factor, "factor", torch.float32, 1)
     _same_count(g, dst)
-    _on("nshb_scale_grads", g, (("factor", factor), ("dst", dst)), stream, _arg(g), _arg(dst), _n(g), _ptr(factor))
+    at = getattr(g, "_index", None)
+    _call("nshb_scale_grads", at, stream, _arg(g), _arg(dst, nshb_tensor, at, "dst"), _n(g),
+          _buffer(factor, "factor", at, torch.float32, 1))
 
 
 def _same_count(a, b) -> None:
@@ -519,16 +523,17 @@ def fp4_quantize(x, q, ws=None, transpose: bool = False, stream=None):
     (tensor_workspace(x)) is needed for NSHB_NVFP4."""
     if _n(x) != _n(q):
         raise ValueError(f"{_n(q)} 4-bit matrices for {_n(x)} tensors")
-    ptr, nbytes = (None, 0) if ws is None else _ws(ws)
-    _on("nshb_fp4_quantize", x, (("q", q), ("workspace", ws)), stream,
-        _arg(x), _arg(q, nshb_fp4), _n(x), 1 if transpose else 0, ptr, nbytes)
+    at = getattr(x, "_index", None)
+    _call("nshb_fp4_quantize", at, stream, _arg(x), _arg(q, nshb_fp4, at, "q"), _n(x), 1 if transpose else 0,
+          *((None, 0) if ws is None else _workspace(ws, at)))
 
 
 def fp4_dequantize(q, x, stream=None):
     """The values of the 4-bit matrices `q` into the tensors `x`."""
     if _n(x) != _n(q):
         raise ValueError(f"{_n(x)} tensors for {_n(q)} 4-bit matrices")
-    _on("nshb_fp4_dequantize", q, (("x", x),), stream, _arg(q, nshb_fp4), _arg(x), _n(q))
+    at = getattr(q, "_index", None)
+    _call("nshb_fp4_dequantize", at, stream, _arg(q, nshb_fp4), _arg(x, nshb_tensor, at, "x"), _n(q))
 
 
 def fp4_matmul(a, b, d, ws, stream=None):
@@ -536,9 +541,9 @@ def fp4_matmul(a, b, d, ws, stream=None):
     matrices a[i] a[i]^T.  `ws`: tensor_workspace(d)."""
     if _n(a) != _n(d) or (b is not None and _n(b) != _n(d)):
         raise ValueError(f"{_n(a)} and {_n(b) if b is not None else _n(a)} operands for {_n(d)} results")
-    ptr, nbytes = _ws(ws)
-    _on("nshb_fp4_matmul", d, (("a", a), ("b", b), ("workspace", ws)), stream,
-        _arg(a, nshb_fp4), _arg(b, nshb_fp4), _arg(d), _n(d), ptr, nbytes)
+    at = getattr(d, "_index", None)
+    _call("nshb_fp4_matmul", at, stream, _arg(a, nshb_fp4, at, "a"), _arg(b, nshb_fp4, at, "b"), _arg(d), _n(d),
+          *_workspace(ws, at))
 
 
 def device_status(ws, stream=None) -> int:
