@@ -79,7 +79,8 @@ int64_t count_tiles(int64_t p, int64_t q, int bm, int bn, bool sym) {
   return n;
 }
 
-Shape shape_of(int64_t m, int64_t n, int64_t kt, bool sym, bool pairs) {
+// pairs: the call has CTA pairs for half of the GPU; narrow: all its tiles, 64 columns wide, fit the GPU at once.
+Shape shape_of(int64_t m, int64_t n, int64_t kt, bool sym, bool pairs, bool narrow, int64_t sms) {
   Shape s = {128, 1, false, 0};
   if (pairs && kt > 0 && std::min(m, n) > 128) {
     s.bn = kFp4PairBn;
@@ -97,18 +98,17 @@ Shape shape_of(int64_t m, int64_t n, int64_t kt, bool sym, bool pairs) {
   // (128 x 128): split long sums of few tiles.  Measured: 1 x 2048 x 6144 in 8.5 us with 1 CTA a tile, 5.0 with
   // 4, 4.5 with 8; 128 x 2048 x 8192 in 13.3, 8.7 and 9.9 us; but 1 x 6144 x 2048 in 4.1 and 4.8 us,
   // 1024^3 in 5.2 and 9.1 us with 1 and 4.
-  const int64_t sms = device_sms();
   const bool wide_tile = s.bn == 128;
   if (kt >= (wide_tile ? 32 : 24) && s.tiles * 8 <= (wide_tile ? sms / 2 : sms)) s.split = 8;
   else if (kt >= 16 && s.tiles * 4 <= sms) s.split = 4;
   else if (kt >= (wide_tile ? 32 : 16) && s.tiles * 2 <= sms) s.split = 2;
-  // Few tiles without a cluster: half as wide ones spread the epilogue over twice the CTAs.
-  if (wide_tile && s.split == 1) {
-    const int64_t narrow = count_tiles(p, q, 128, 64, sym);
-    if (narrow <= sms) {
-      s.bn = 64;
-      s.tiles = narrow;
-    }
+  // Few tiles without a cluster: half as wide ones spread the epilogue over twice the CTAs.  Measured (128 and 64
+  // columns): 1000 x 777 x 1333 to fp32 8.5 and 7.0 us, 768 x 768 x 1000 6.8 and 5.8 us, its Gram matrix 7.6 and
+  // 7.0 us, 1024^3 to bf16 4.9 and 4.6 us; two CTAs of an SM hide each other's epilogue as well: eight of 512 x 512 x
+  // 2048 (256 tiles) 7.6 and 6.8 us, but in two waves 16 of them 8.5 and 12.9 us.
+  if (narrow && wide_tile && s.split == 1) {
+    s.bn = 64;
+    s.tiles = count_tiles(p, q, 128, 64, sym);
   }
   return s;
 }
@@ -133,68 +133,88 @@ nshb_status check_products(const nshb_fp4 *A, const nshb_fp4 *B, const nshb_tens
 // Products of one launch; `d` as the caller stores it.  See launch_fp4_gemm for what the launches share.
 nshb_status run_fp4_products(const nshb_fp4 *A, const nshb_fp4 *B, const nshb_tensor *D, int32_t n, uint32_t *status,
                              bool clear, long long limit, cudaStream_t st) {
-  int64_t wide = 0;   // tiles of CTA pairs in the call
+  const int64_t sms = device_sms();
+  int64_t wide = 0, few = 0;   // tiles of CTA pairs, CTAs with the narrowest tiles in the call
+  auto shape = [&](int32_t i, bool pairs, bool narrow) {
+    return shape_of(D[i].rows, D[i].cols, (A[i].cols + 255) / 256, !B, pairs, narrow, sms);
+  };
   for (int32_t i = 0; i < n; ++i)
     if (D[i].rows && D[i].cols) {
-      const Shape s = shape_of(D[i].rows, D[i].cols, (A[i].cols + 255) / 256, !B, true);
+      const Shape s = shape(i, true, false), t = shape(i, false, true);
       wide += s.bn == kFp4PairBn ? s.tiles : 0;
+      few += t.tiles * t.split;
     }
-  const bool pairs = wide >= device_sms() / 2;
-  int32_t i = 0;
-  while (i < n) {
-    Fp4GemmParams p;
-    std::memset(static_cast<Fp4GemmHead *>(&p), 0, sizeof(Fp4GemmHead));
-    p.status = status;
-    p.wait_limit = limit;
-    p.clear_status = clear;
-    Shape first = {0, 0, false, 0};
-    int32_t format = 0;
-    int64_t tiles = 0;
-    for (; i < n && p.nprob < kMaxFp4Prob; ++i) {
-      const nshb_fp4 &a = A[i], &b = B ? B[i] : A[i];
-      if (D[i].rows == 0 || D[i].cols == 0) continue;
-      const int64_t kt = (a.cols + 255) / 256;
-      const bool sym = !B;
-      const Shape s = shape_of(D[i].rows, D[i].cols, kt, sym, pairs);
-      if (p.nprob && (s.bn != first.bn || s.split != first.split || a.format != format)) break;
-      if ((tiles + s.tiles) * s.split > (1LL << 30)) {
-        if (p.nprob) break;
-        return NSHB_ERR_UNSUPPORTED;
-      }
-      first = s;
-      format = a.format;
-      Fp4Prob &q = p.prob[p.nprob++];
-      std::memset(&q, 0, sizeof(q));
-      const nshb_fp4 &P = s.swap ? b : a, &Q = s.swap ? a : b;
-      if (kt) {
-        const bool pair = s.bn == kFp4PairBn;
-        cudaError_t e = encode_fp4_maps(&q.pc, &q.ps, P, 128, 1, 1);
-        if (e == cudaSuccess) e = encode_fp4_maps(&q.qc, &q.qs, Q, pair ? 128 : s.bn, 1, pair ? 2 : 1);
-        if (e != cudaSuccess) {
-          record_cuda_error(e);
-          return NSHB_ERR_CUDA;
+  const bool pairs = wide >= sms / 2, narrow = few <= 2 * sms;
+  // A launch takes the products of one kind (shape and format), wherever they stand in the list: 32 products of four
+  // kinds in turn take 50 us, in launches of neighbours 147 us.
+  auto log2 = [](int v) {
+    int k = 0;
+    while (v >>= 1) ++k;
+    return k;
+  };
+  auto kind_of = [&](const Shape &s, int32_t i) {   // bn from 16 to 256, split up to 8
+    return 8 * log2(s.bn / 16) + 2 * log2(s.split) + (A[i].format == NSHB_NVFP4);
+  };
+  uint64_t kinds = 0;
+  for (int32_t i = 0; i < n; ++i)
+    if (D[i].rows && D[i].cols) kinds |= 1ull << kind_of(shape(i, pairs, narrow), i);
+  for (int kind = 0; kinds >> kind; ++kind) {
+    if (!(kinds >> kind & 1)) continue;
+    for (int32_t i = 0; i < n;) {
+      Fp4GemmParams p;
+      std::memset(static_cast<Fp4GemmHead *>(&p), 0, sizeof(Fp4GemmHead));
+      p.status = status;
+      p.wait_limit = limit;
+      p.clear_status = clear;
+      Shape first = {0, 0, false, 0};
+      int32_t format = 0;
+      int64_t tiles = 0;
+      for (; i < n && p.nprob < kMaxFp4Prob; ++i) {
+        const nshb_fp4 &a = A[i], &b = B ? B[i] : A[i];
+        if (D[i].rows == 0 || D[i].cols == 0) continue;
+        const int64_t kt = (a.cols + 255) / 256;
+        const bool sym = !B;
+        const Shape s = shape(i, pairs, narrow);
+        if (kind_of(s, i) != kind) continue;
+        if ((tiles + s.tiles) * s.split > (1LL << 30)) {
+          if (p.nprob) break;
+          return NSHB_ERR_UNSUPPORTED;
         }
-        if (a.format == NSHB_NVFP4) {
-          q.pg = P.global;
-          q.qg = Q.global;
+        first = s;
+        format = a.format;
+        Fp4Prob &q = p.prob[p.nprob++];
+        std::memset(&q, 0, sizeof(q));
+        const nshb_fp4 &P = s.swap ? b : a, &Q = s.swap ? a : b;
+        if (kt) {
+          const bool pair = s.bn == kFp4PairBn;
+          cudaError_t e = encode_fp4_maps(&q.pc, &q.ps, P, 128, 1, 1);
+          if (e == cudaSuccess) e = encode_fp4_maps(&q.qc, &q.qs, Q, pair ? 128 : s.bn, 1, pair ? 2 : 1);
+          if (e != cudaSuccess) {
+            record_cuda_error(e);
+            return NSHB_ERR_CUDA;
+          }
+          if (a.format == NSHB_NVFP4) {
+            q.pg = P.global;
+            q.qg = Q.global;
+          }
         }
+        const bool f32 = D[i].dtype == NSHB_F32;
+        q.d = D[i].data;
+        q.ld = D[i].rows == 1 ? D[i].cols : D[i].ld;
+        q.np = (int32_t)(s.swap ? D[i].cols : D[i].rows);
+        q.nq = (int32_t)(s.swap ? D[i].rows : D[i].cols);
+        q.kt = (int32_t)kt;
+        q.qtiles = (q.nq + s.bn - 1) / s.bn;
+        q.tile_begin = (int32_t)tiles;
+        const bool vec = (uintptr_t)D[i].data % 16 == 0 && (D[i].rows == 1 || (q.ld * (f32 ? 4 : 2)) % 16 == 0);
+        q.flags = (s.swap ? kFp4DTrans : 0) | (f32 ? kFp4DF32 : 0) | (sym ? kFp4Sym : 0) | (vec ? kFp4DVec : 0);
+        tiles += s.tiles;
       }
-      const bool f32 = D[i].dtype == NSHB_F32;
-      q.d = D[i].data;
-      q.ld = D[i].rows == 1 ? D[i].cols : D[i].ld;
-      q.np = (int32_t)(s.swap ? D[i].cols : D[i].rows);
-      q.nq = (int32_t)(s.swap ? D[i].rows : D[i].cols);
-      q.kt = (int32_t)kt;
-      q.qtiles = (q.nq + s.bn - 1) / s.bn;
-      q.tile_begin = (int32_t)tiles;
-      const bool vec = (uintptr_t)D[i].data % 16 == 0 && (D[i].rows == 1 || (q.ld * (f32 ? 4 : 2)) % 16 == 0);
-      q.flags = (s.swap ? kFp4DTrans : 0) | (f32 ? kFp4DF32 : 0) | (sym ? kFp4Sym : 0) | (vec ? kFp4DVec : 0);
-      tiles += s.tiles;
+      if (!p.nprob) break;
+      p.total_tiles = (int32_t)tiles;
+      NSHB_RUN(NSHB_PROF_FP4, launch_fp4_gemm(p, first.bn, first.split, format == NSHB_NVFP4, st));
+      clear = false;
     }
-    if (!p.nprob) break;
-    p.total_tiles = (int32_t)tiles;
-    NSHB_RUN(NSHB_PROF_FP4, launch_fp4_gemm(p, first.bn, first.split, format == NSHB_NVFP4, st));
-    clear = false;
   }
   if (clear) NSHB_RUN(NSHB_PROF_FP4, cudaMemsetAsync(status, 0, sizeof(uint32_t), st));
   return NSHB_OK;

@@ -138,6 +138,20 @@ def test_a_list(fmt):
     assert bool((out == 0).all())
 
 
+@pytest.mark.parametrize("gram", [False, True])
+def test_shapes_and_formats_in_turn(gram):
+    """More products of one kind than a launch takes, others between them, both formats and result types."""
+    shapes = ([(130, 140, 64)] * 5 + [(1, 200, 300), (40, 130, 5000), (700, 800, 256), (0, 9, 70), (300, 310, 8200)]) * 11
+    fmts = [MX if i % 3 else NV for i in range(len(shapes))]
+    a = [operand(m, k, f, 10 + i) for i, ((m, n, k), f) in enumerate(zip(shapes, fmts))]
+    b = a if gram else [operand(n, k, f, 500 + i) for i, ((m, n, k), f) in enumerate(zip(shapes, fmts))]
+    for dtype in (torch.float32, torch.bfloat16):
+        ds = product([x[0] for x in a], None if gram else [x[0] for x in b], dtype)
+        for d, x, y, (m, n, k) in zip(ds, a, b, shapes):
+            if m:
+                check(d, x[1], y[1], k)
+
+
 @pytest.mark.parametrize("fmt", [MX, NV])
 @pytest.mark.parametrize("m", [2, 200])
 def test_nan_blocks_reach_their_row_and_no_other(fmt, m):
