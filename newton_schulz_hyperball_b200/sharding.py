@@ -243,6 +243,8 @@ class ShardedOptimizer:
         with torch.cuda.stream(stream):      # the collective and the factor on the step's stream
             if self.mats is not None:
                 self.nshb.grad_norm(self.grads, self.grad_total, self.grad_ws, max_norm=self.max_grad_norm)
+            else:
+                self.grad_total.zero_()      # nothing owned: not the last step's norm over the ranks
             if self.plan.world > 1:
                 norm = global_grad_norm(self.grad_total[:1], self.group)
                 self.grad_total.copy_(torch.cat((norm, clip_factor(norm, self.max_grad_norm))))
