@@ -18,6 +18,7 @@ memory before any kernel reads it.
 """
 from __future__ import annotations
 
+import contextlib
 import heapq
 from dataclasses import dataclass
 
@@ -229,18 +230,37 @@ class ShardedOptimizer:
             self.ws = nshb.workspace(self.mats, self.p, op, device=dev)
 
     def step(self, grads, stream=None) -> None:
-        """One step with this rank's gradients of every matrix (`grads`, in matrix order)."""
-        reduce_scatter_grads(grads, self.plan, self.G, self.group, self.average)
-        if self.max_grad_norm is not None:
-            self.measure_grads(stream)
-        self.local_step(stream)
-        all_gather_weights(self.W, self.plan, self.group)
+        """One step with this rank's gradients of every matrix (`grads`, in matrix order), all of it on `stream` (a
+        torch stream or its pointer; None: the current stream).  It starts after what the current stream holds, the
+        gradients among it, and the current stream goes on after it."""
+        with self._on(stream):
+            reduce_scatter_grads(grads, self.plan, self.G, self.group, self.average)
+            if self.max_grad_norm is not None:
+                self.measure_grads()
+            self.local_step()
+            all_gather_weights(self.W, self.plan, self.group)
+
+    @contextlib.contextmanager
+    def _on(self, stream):
+        if stream is None:
+            yield
+            return
+        if isinstance(stream, int):
+            dev = self.W[0].device
+            stream = torch.cuda.ExternalStream(stream, device=dev) if stream else torch.cuda.default_stream(dev)
+        caller = torch.cuda.current_stream(stream.device)
+        if stream != caller:
+            stream.wait_stream(caller)
+        try:
+            with torch.cuda.stream(stream):
+                yield
+        finally:
+            if stream != caller:
+                caller.wait_stream(stream)
 
     def measure_grads(self, stream=None) -> None:
-        """(norm, clip factor) of all ranks' reduced gradients into grad_total."""
-        if isinstance(stream, int):
-            stream = torch.cuda.ExternalStream(stream)
-        with torch.cuda.stream(stream):      # the collective and the factor on the step's stream
+        """(norm, clip factor) of all ranks' reduced gradients into grad_total; `stream` as in step."""
+        with self._on(stream):
             if self.mats is not None:
                 self.nshb.grad_norm(self.grads, self.grad_total, self.grad_ws, max_norm=self.max_grad_norm)
             else:
@@ -251,7 +271,7 @@ class ShardedOptimizer:
 
     def local_step(self, stream=None) -> None:
         """The library's step on the owned matrices, with the gradients already in self.G (and with
-        max_grad_norm their norm in grad_total)."""
+        max_grad_norm their norm in grad_total).  Waits for nothing but what `stream` holds."""
         if self.mats is None:
             return
         if self.max_grad_norm is not None:
