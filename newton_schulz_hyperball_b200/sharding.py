@@ -158,7 +158,8 @@ def reduce_scatter_grads(grads, plan: ShardPlan, out, group=None, average: bool 
 def clip_factor(norm, max_norm: float):
     """min(1, max_norm / (norm + 1e-6)) in fp32, 0 for an infinite norm, NaN for a NaN one: what the library's
     nshb_grad_norm writes next to the norm."""
-    f = (max_norm / (norm.float() + 1e-6)).clamp(max=1.0)
+    norm = norm.float()
+    f = (torch.full_like(norm, max_norm) / (norm + 1e-6)).clamp(max=1.0)    # scalar / tensor rounds twice
     return torch.where(torch.isinf(norm), torch.zeros_like(f), f)
 
 
