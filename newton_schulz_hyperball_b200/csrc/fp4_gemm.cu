@@ -78,6 +78,32 @@ __device__ __forceinline__ void tile_of(const Fp4Prob &q, int l, int &pt, int &q
   }
 }
 
+// What the accumulator's elements are multiplied with: the product of the matrices' scales, or where that
+// leaves fp32's normal range (scales near 2^-77, 2^70) both one after the other, the larger first, so that nothing that
+// D can hold is lost and no zero becomes 0 x infinity.  The second is read again where it is needed: the epilogue has no
+// register for it.
+struct MatrixScales {
+  float a = 1.f;
+  bool two = false;
+  __device__ __forceinline__ explicit MatrixScales(const Fp4Prob &q) {
+    if (!q.pg) return;
+    const float x = *q.pg, y = *q.qg;
+    a = x * y;
+    two = !(isfinite(a) && (fabsf(a) >= 0x1p-126f || x == 0.f || y == 0.f));
+    if (two) a = fabsf(x) >= fabsf(y) ? x : y;
+  }
+  template <int N>
+  __device__ __forceinline__ void apply(const Fp4Prob &q, float (&v)[N]) const {
+#pragma unroll
+    for (int e = 0; e < N; ++e) v[e] *= a;
+    if (two) {
+      const float x = *q.pg, y = *q.qg, b = fabsf(x) >= fabsf(y) ? y : x;
+#pragma unroll
+      for (int e = 0; e < N; ++e) v[e] *= b;
+    }
+  }
+};
+
 // N values of D: row p, columns q0 .. q0 + N - 1 of the tile's orientation.
 template <int N>
 __device__ __forceinline__ void store_row(const Fp4Prob &q, int64_t p, int64_t q0, const float (&v)[N], bool trans) {
@@ -317,7 +343,7 @@ __global__ void __launch_bounds__(kThreads, 2) fp4_gemm_kernel(const __grid_cons
   const int row = quarter * 32 + lane;
   const bool epi = warp >= 2;
   bool have = k1 > k0;
-  const float g = q.pg ? *q.pg * *q.qg : 1.f;
+  const MatrixScales g(q);
   const bool trans = q.flags & kFp4DTrans, sym = q.flags & kFp4Sym;
   constexpr int N = BN < 32 ? BN : 32;
   if (epi && have && !mbar_wait_warp(done, 0, limit)) {
@@ -335,8 +361,7 @@ __global__ void __launch_bounds__(kThreads, 2) fp4_gemm_kernel(const __grid_cons
     for (int e = 0; e < N; ++e) v[e] = __uint_as_float(r[e]);
   };
   auto store = [&](int c, float (&v)[N]) {
-#pragma unroll
-    for (int e = 0; e < N; ++e) v[e] *= g;
+    g.apply(q, v);
     const int64_t at = (int64_t)qt * BN + c;
     if constexpr (N == 32) {
       // the ring is free: this CTA's MMAs are done
@@ -398,8 +423,7 @@ __global__ void __launch_bounds__(kThreads, 2) fp4_gemm_kernel(const __grid_cons
 #pragma unroll
           for (int e = 0; e < W; ++e) v[e] += ld_cluster(from + 512u * e);
         }
-#pragma unroll
-        for (int e = 0; e < W; ++e) v[e] *= g;
+        g.apply(q, v);
         store_row<W>(q, (int64_t)pt * 128 + row, (int64_t)qt * BN + c, v, true);
       };
       const int each = BN / parts, c0 = each * part;
@@ -420,7 +444,9 @@ __global__ void __launch_bounds__(kThreads, 2) fp4_gemm_kernel(const __grid_cons
           const float4 x = ld_cluster4(mapa(base + (uint32_t)(((r0 + r) * kPitch + c) * 4), (uint32_t)k));
           v.x += x.x; v.y += x.y; v.z += x.z; v.w += x.w;
         }
-        *reinterpret_cast<float4 *>(sum + r * kPitch + c) = make_float4(g * v.x, g * v.y, g * v.z, g * v.w);
+        float o[4] = {v.x, v.y, v.z, v.w};
+        g.apply(q, o);
+        *reinterpret_cast<float4 *>(sum + r * kPitch + c) = make_float4(o[0], o[1], o[2], o[3]);
       }
       named_barrier(1, 32 * kEpiWarps);
       const int64_t p0 = (int64_t)pt * 128 + r0, q0 = (int64_t)qt * BN;
@@ -639,7 +665,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) fp4_pair_kernel(const __grid_
       const Fp4Prob &q = p.prob[find_prob(p, tile)];
       int pt, qt;
       tile_of<256, 256>(q, tile - q.tile_begin, pt, qt);
-      const float g = q.pg ? *q.pg * *q.qg : 1.f;
+      const MatrixScales g(q);
       const int64_t row = (int64_t)pt * 256 + 128 * rank + quarter * 32 + lane;
       const uint32_t acc = tmem + (uint32_t)((tl & 1) * C::kShift) + ((uint32_t)(quarter * 32) << 16);
       // 32 columns at a time: one of the two shared chunks first, then three others
@@ -662,7 +688,8 @@ __global__ void __launch_bounds__(kPairThreads, 1) fp4_pair_kernel(const __grid_
         }
         float v[32];
 #pragma unroll
-        for (int e = 0; e < 32; ++e) v[e] = g * __uint_as_float(r[e]);
+        for (int e = 0; e < 32; ++e) v[e] = __uint_as_float(r[e]);
+        g.apply(q, v);
         const int64_t c = (int64_t)qt * 256 + cc;
         store_block(q, out + 2048 * (warp - 2), row - lane, c, v);
         if (q.flags & kFp4Sym) store_mirror(q, row, c, v);
