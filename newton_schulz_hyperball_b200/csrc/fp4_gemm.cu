@@ -199,21 +199,30 @@ __device__ __forceinline__ void store_block(const Fp4Prob &q, uint8_t *stage, in
   }
 }
 
-// The mirror image of such a block's elements below the diagonal.
-__device__ __forceinline__ void store_mirror(const Fp4Prob &q, int64_t row, int64_t c, const float (&v)[32]) {
-  const int64_t row0 = row - (threadIdx.x & 31);
-  if (c >= row0 + 31 || row >= q.np) return;
-  const bool whole = c + 31 < row0 && c + 32 <= q.nq;   // else the block crosses the diagonal or D's end
+// Such a block of a symmetric result; row0 and c are multiples of 32.  Blocks below the diagonal are stored with
+// their mirror image, those above it not at all, of those on it the elements up to the diagonal with theirs: each
+// element of D has one writer, and (i, j) has the bits of (j, i).
+__device__ __forceinline__ void store_symmetric(const Fp4Prob &q, uint8_t *stage, int64_t row0, int64_t c, const float (&v)[32]) {
+  if (c > row0) return;
+  const bool on = c == row0;
+  if (!on) store_block(q, stage, row0, c, v);
+  const int64_t row = row0 + (threadIdx.x & 31);
+  if (row >= q.np) return;
+  const int n = on ? (int)(row - c) : 32;              // the elements below the diagonal
   if (q.flags & kFp4DF32) {
-    float *d = static_cast<float *>(q.d) + c * q.ld + row;
+    float *d = static_cast<float *>(q.d) + c * q.ld + row, *r = static_cast<float *>(q.d) + row * q.ld + c;
 #pragma unroll
-    for (int e = 0; e < 32; ++e, d += q.ld)
-      if (whole || (c + e < row && c + e < q.nq)) *d = v[e];
+    for (int e = 0; e < 32; ++e, d += q.ld) {
+      if (e < n) *d = v[e];
+      if (on && e <= n) r[e] = v[e];
+    }
   } else {
-    __nv_bfloat16 *d = static_cast<__nv_bfloat16 *>(q.d) + c * q.ld + row;
+    __nv_bfloat16 *d = static_cast<__nv_bfloat16 *>(q.d) + c * q.ld + row, *r = static_cast<__nv_bfloat16 *>(q.d) + row * q.ld + c;
 #pragma unroll
-    for (int e = 0; e < 32; ++e, d += q.ld)
-      if (whole || (c + e < row && c + e < q.nq)) *d = __float2bfloat16_rn(v[e]);
+    for (int e = 0; e < 32; ++e, d += q.ld) {
+      if (e < n) *d = __float2bfloat16_rn(v[e]);
+      if (on && e <= n) r[e] = __float2bfloat16_rn(v[e]);
+    }
   }
 }
 
@@ -365,9 +374,11 @@ __global__ void __launch_bounds__(kThreads, 2) fp4_gemm_kernel(const __grid_cons
     const int64_t at = (int64_t)qt * BN + c;
     if constexpr (N == 32) {
       // the ring is free: this CTA's MMAs are done
-      if (!trans) store_block(q, smem + 2048 * (warp - 2), (int64_t)pt * 128 + 32 * quarter, at, v);
-      else store_row<N>(q, (int64_t)pt * 128 + row, at, v, true);
-      if (sym) store_mirror(q, (int64_t)pt * 128 + row, at, v);
+      uint8_t *stage = smem + 2048 * (warp - 2);
+      const int64_t row0 = (int64_t)pt * 128 + 32 * quarter;
+      if (sym) store_symmetric(q, stage, row0, at, v);
+      else if (!trans) store_block(q, stage, row0, at, v);
+      else store_row<N>(q, row0 + lane, at, v, true);
     } else {
       store_row<N>(q, (int64_t)pt * 128 + row, at, v, trans);
     }
@@ -452,7 +463,8 @@ __global__ void __launch_bounds__(kThreads, 2) fp4_gemm_kernel(const __grid_cons
       const int64_t p0 = (int64_t)pt * 128 + r0, q0 = (int64_t)qt * BN;
       const int rows = (int)(q.np - p0 < n ? q.np - p0 : n), cols = (int)(q.nq - q0 < BN ? q.nq - q0 : BN);
       const bool f32 = q.flags & kFp4DF32;
-      if ((q.flags & kFp4DVec) && cols == BN) {
+      const bool on = sym && pt == qt;                    // a tile on the diagonal: see store_symmetric
+      if ((q.flags & kFp4DVec) && cols == BN && !on) {
         for (int i = w * kRows; i < rows; i += kEpiWarps * kRows) {
           const int r = i + lane / L, c = 4 * (lane % L);
           const float4 x = *reinterpret_cast<const float4 *>(sum + r * kPitch + c);
@@ -463,16 +475,17 @@ __global__ void __launch_bounds__(kThreads, 2) fp4_gemm_kernel(const __grid_cons
         }
       } else {
         for (int r = w; r < rows; r += kEpiWarps)
-          for (int c = lane; c < cols; c += 32) {
+          for (int c = lane; c < (on ? r0 + r + 1 : cols); c += 32) {
             const int64_t at = (p0 + r) * q.ld + q0 + c;
             if (f32) static_cast<float *>(q.d)[at] = sum[r * kPitch + c];
             else static_cast<__nv_bfloat16 *>(q.d)[at] = __float2bfloat16_rn(sum[r * kPitch + c]);
           }
       }
-      if (sym && pt != qt) {
+      if (sym) {
         // the mirror image: rows run along D's columns
         for (int c = w; c < cols; c += kEpiWarps)
           for (int r = lane; r < rows; r += 32) {
+            if (on && c >= r0 + r) continue;
             const int64_t at = (q0 + c) * q.ld + p0 + r;
             if (f32) static_cast<float *>(q.d)[at] = sum[r * kPitch + c];
             else static_cast<__nv_bfloat16 *>(q.d)[at] = __float2bfloat16_rn(sum[r * kPitch + c]);
@@ -666,7 +679,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) fp4_pair_kernel(const __grid_
       int pt, qt;
       tile_of<256, 256>(q, tile - q.tile_begin, pt, qt);
       const MatrixScales g(q);
-      const int64_t row = (int64_t)pt * 256 + 128 * rank + quarter * 32 + lane;
+      const int64_t row0 = (int64_t)pt * 256 + 128 * rank + quarter * 32;
       const uint32_t acc = tmem + (uint32_t)((tl & 1) * C::kShift) + ((uint32_t)(quarter * 32) << 16);
       // 32 columns at a time: one of the two shared chunks first, then three others
       const int shared_c = ((tl & 1) ? 0 : C::kShift) + 32 * half, rest_c = ((tl & 1) ? C::kShared : 0) + 96 * half;
@@ -691,8 +704,8 @@ __global__ void __launch_bounds__(kPairThreads, 1) fp4_pair_kernel(const __grid_
         for (int e = 0; e < 32; ++e) v[e] = __uint_as_float(r[e]);
         g.apply(q, v);
         const int64_t c = (int64_t)qt * 256 + cc;
-        store_block(q, out + 2048 * (warp - 2), row - lane, c, v);
-        if (q.flags & kFp4Sym) store_mirror(q, row, c, v);
+        if (q.flags & kFp4Sym) store_symmetric(q, out + 2048 * (warp - 2), row0, c, v);
+        else store_block(q, out + 2048 * (warp - 2), row0, c, v);
       }
       tc_fence_before();
     }
