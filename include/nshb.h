@@ -365,8 +365,8 @@ nshb_status nshb_fp4_dequantize(const nshb_fp4 *Q, const nshb_tensor *X, int32_t
 
 /* D[i] = A[i] B[i]^T (rows of A x rows of B, bf16 or fp32, any ld), or with B == NULL the Gram matrix
  * A[i] A[i]^T (both triangles): products of 4-bit matrices of one format and equal cols on the tensor
- * cores, fp32 accumulation, multiplied by both global scales and rounded once.  cols == 0 gives
- * zeros.  A NaN scale makes the rows (columns) of D that use it NaN.  No D overlaps an
+ * cores, fp32 accumulation, multiplied by both global scales in fp32, then rounded to D's dtype.  cols == 0
+ * gives zeros.  A NaN scale makes the rows (columns) of D that use it NaN.  No D overlaps an
  * operand or another D.  The tensor cores read the operands in place.  Any sizes from one row (a single token) on;
  * the number of CTAs that share a sum, and so its order, depends on the sizes of the call's matrices and the
  * GPU's number of SMs alone.
