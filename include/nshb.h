@@ -339,7 +339,9 @@ nshb_status nshb_scale_grads(const nshb_tensor *src, const nshb_tensor *dst, int
  *         aligned; zero past cols.
  * scales: tiles of 128 rows x 4 scales (512 bytes, 16-byte aligned), tile (i, j) at index
  *         i * tiles_per_row + j with tiles_per_row = round_up(cols, 128) / (4 * block); scale (r, s) of a
- *         tile at byte 16 (r mod 32) + 4 (r div 32) + s: the order in which the tensor core reads them.
+ *         tile at byte 16 (r mod 32) + 4 (r div 32) + s: the order in which the tensor core reads them.  E4M3's
+ *         sign bit is zero.  Bytes past cols are zero (the products multiply their zero codes by them), those past
+ *         rows are any.  nshb_fp4_quantize writes zeros in both.
  * nshb_fp4_size gives the bytes of both.  rows and cols up to 2^24; 0 allowed (nothing is read or written). */
 typedef enum { NSHB_MXFP4 = 0, NSHB_NVFP4 = 1 } nshb_fp4_format;
 struct nshb_fp4 {

@@ -831,10 +831,18 @@ nshb_status run_newton_precond(const nshb_matrix *mats, const Plan &pl, const ns
     NSHB_LAUNCH(NSHB_PROF_MOMENTUM, launch_momentum(mp, st));
   }
   // 2. S = Z Z^T on the tensor cores (fp32 out), its operands read straight from each Z (4-bit: both
-  //    triangles, zeros in the padding like the other)
+  //    triangles of the d x d part, and zeros around it)
   if (Zq) {
     nshb_tensor S[kMaxMats];
-    for (int j = 0; j < nz; ++j) S[j] = {pl.zp[j].Dp, pl.zp[j].Dp, pl.zp[j].Dp, NSHB_F32, 0, ws + pl.zp[j].s};
+    for (int j = 0; j < nz; ++j) {
+      const Plan::ZPlan &z = pl.zp[j];
+      char *s = ws + z.s;
+      S[j] = {z.d, z.d, z.Dp, NSHB_F32, 0, s};
+      if (z.d == z.Dp) continue;
+      const size_t row = (size_t)z.Dp * 4, pad = (size_t)(z.Dp - z.d);
+      NSHB_CHECK_CUDA(cudaMemset2DAsync(s + z.d * 4, row, 0, pad * 4, (size_t)z.d, st));
+      NSHB_CHECK_CUDA(cudaMemsetAsync(s + z.d * row, 0, pad * row, st));
+    }
     const nshb_status e = run_fp4_products(Zq, nullptr, S, nz, status, /*clear=*/false, limit, st);
     if (e != NSHB_OK) return e;
   }

@@ -19,7 +19,7 @@ namespace nshb {
 namespace {
 
 // lambda = ridge_rel tr(S) / d added to the diagonal.  The padded rows and columns of S
-// (d .. ld-1, zero from the Gram) get a unit diagonal, so the padded matrix factors as
+// (d .. ld-1, zero before) get a unit diagonal, so the padded matrix factors as
 // [L 0; 0 I] and the padded columns of every solve stay zero.
 __global__ void __launch_bounds__(256) ridge_kernel(const __grid_constant__ CholParams p) {
   __shared__ double red[8];

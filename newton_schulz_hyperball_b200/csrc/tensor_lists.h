@@ -40,8 +40,7 @@ nshb_status run_largest(const nshb_tensor *t, int32_t n, const TensWorkspace &w,
 constexpr int64_t kMaxFp4Dim = 1LL << 24;
 nshb_status check_fp4(const nshb_fp4 &q);
 constexpr long long kFp4WaitLimit = 4000000000LL;   // ~2 s of SM clock per barrier phase
-// D[i] = A[i] B[i]^T (B NULL: A[i] A[i]^T) for checked arguments; D may have more rows and columns than the
-// operands have rows (zeros there).
+// D[i] = A[i] B[i]^T (B NULL: A[i] A[i]^T) for checked arguments.
 nshb_status run_fp4_products(const nshb_fp4 *A, const nshb_fp4 *B, const nshb_tensor *D, int32_t n, uint32_t *status,
                              bool clear, long long limit, cudaStream_t st);
 
