@@ -14,7 +14,7 @@ namespace nshb {
 // Sizes, limits, dtype, pointer and alignment of one tensor, in this order.
 nshb_status check_tensor(const nshb_tensor &t) {
   if (t.rows < 0 || t.cols < 0 || (t.rows > 1 && t.ld < t.cols)) return NSHB_ERR_SHAPE;
-  if (t.rows > (1LL << 40) || t.cols > (1LL << 40) || t.ld > (1LL << 40)) return NSHB_ERR_UNSUPPORTED;
+  if (t.rows > (1LL << 40) || t.cols > (1LL << 40) || (t.rows > 1 && t.ld > (1LL << 40))) return NSHB_ERR_UNSUPPORTED;
   if (t.dtype != NSHB_BF16 && t.dtype != NSHB_F32) return NSHB_ERR_DTYPE;
   if (t.reserved != 0) return NSHB_ERR_PARAM;
   if (t.rows == 0 || t.cols == 0) return NSHB_OK;
