@@ -282,7 +282,8 @@ nshb_status nshb_fro_norms_static(const nshb_matrix *mats, int32_t n_mats, float
  * ld is not looked at for one row).  rows or cols may be 0: the tensor then has no elements and
  * its pointer is not looked at.  `data` must be aligned to its element.  Tensors whose rows
  * follow one another (ld == cols, or one row) are read as one run of elements whatever their
- * alignment; sizes up to 2^40 elements, ld up to 2^40, else NSHB_ERR_UNSUPPORTED. */
+ * alignment; sizes up to 2^40 elements, ld up to 2^40, up to 2^30 rows that do not follow one another, else
+ * NSHB_ERR_UNSUPPORTED. */
 typedef struct {
   int64_t rows, cols, ld;
   int32_t dtype; /* nshb_dtype */

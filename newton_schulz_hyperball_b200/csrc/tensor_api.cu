@@ -21,6 +21,7 @@ nshb_status check_tensor(const nshb_tensor &t) {
   // rows * cols and the last element's offset, without overflow: both factors are at most 2^40
   if (t.rows > (1LL << 40) / t.cols) return NSHB_ERR_UNSUPPORTED;
   if (t.rows > 1 && t.rows > (1LL << 44) / t.ld) return NSHB_ERR_UNSUPPORTED;
+  if (t.rows > kMaxRuns && t.ld != t.cols) return NSHB_ERR_UNSUPPORTED;
   if (!t.data) return NSHB_ERR_NULL;
   if ((uintptr_t)t.data % (t.dtype == NSHB_F32 ? 4 : 2)) return NSHB_ERR_SHAPE;
   return NSHB_OK;
@@ -57,8 +58,8 @@ int tens_ctas(int nwin) { return std::min(nwin, std::min(kTensCtasPerSm * device
 
 namespace {
 
-// One tensor's record: a contiguous tensor is one run whatever its shape.  False where it has
-// too many windows for a launch.
+// One tensor's record: a contiguous tensor is one run whatever its shape.  False where the launch would have too
+// many windows; never for its first tensor (up to 2^30 rows of one window, 2^28 of two, and so on).
 bool fill(const nshb_tensor &s, const nshb_tensor *d, int64_t &win, TensRec &q) {
   const int64_t esz = s.dtype == NSHB_F32 ? 4 : 2, per = kWinBytes / esz;
   int64_t rows = s.rows, cols = s.cols;
@@ -85,7 +86,7 @@ bool fill(const nshb_tensor &s, const nshb_tensor *d, int64_t &win, TensRec &q) 
     q.per_row = (int32_t)(per / cols);
     n = (rows + q.per_row - 1) / q.per_row;
   }
-  if (rows > (1LL << 30) || win + n > (1LL << 30)) return false;
+  if (win + n > (1LL << 30)) return false;
   q.rows = (int32_t)rows;
   win += n;
   return true;
@@ -93,8 +94,7 @@ bool fill(const nshb_tensor &s, const nshb_tensor *d, int64_t &win, TensRec &q) 
 
 // Fills the records of tensors from `i` on, as many as one launch takes; `i` is moved past them.
 // index/win_begin/empties (when given) receive what the finalize kernel needs.
-nshb_status fill_launch(const nshb_tensor *src, const nshb_tensor *dst, int32_t n, int32_t &i, TensParams &p,
-                        TensFinParams *fin) {
+void fill_launch(const nshb_tensor *src, const nshb_tensor *dst, int32_t n, int32_t &i, TensParams &p, TensFinParams *fin) {
   int64_t win = 0;
   int32_t seen = 0;
   int32_t empty[kMaxTens];
@@ -105,10 +105,7 @@ nshb_status fill_launch(const nshb_tensor *src, const nshb_tensor *dst, int32_t 
       empty[n_empty++] = i;
       continue;
     }
-    if (!fill(src[i], dst ? &dst[i] : nullptr, win, p.t[p.ntens])) {
-      if (p.ntens == 0) return NSHB_ERR_UNSUPPORTED;
-      break;
-    }
+    if (!fill(src[i], dst ? &dst[i] : nullptr, win, p.t[p.ntens])) break;
     if (fin) {
       fin->at[p.ntens].index = i;
       fin->at[p.ntens].win_begin = p.t[p.ntens].win_begin;
@@ -124,7 +121,6 @@ nshb_status fill_launch(const nshb_tensor *src, const nshb_tensor *dst, int32_t 
     fin->nwin = p.nwin;
     fin->nctas = p.nctas;
   }
-  return NSHB_OK;
 }
 
 // The whole call in one launch where the list is short.  Otherwise *done stays false and nothing is queued.
@@ -173,8 +169,7 @@ nshb_status run_norm(const nshb_tensor *g, int32_t n, int32_t kind, float max_no
     std::memset(static_cast<TensHead *>(&p), 0, sizeof(TensHead));
     TensFinParams f;
     std::memset(static_cast<TensFinHead *>(&f), 0, sizeof(TensFinHead));
-    const nshb_status e = fill_launch(g, nullptr, n, i, p, &f);
-    if (e != NSHB_OK) return e;
+    fill_launch(g, nullptr, n, i, p, &f);
     p.rec = w.rec;
     p.kind = kind;
     NSHB_RUN(NSHB_PROF_GRAD, launch_tens_norm(p, st));
@@ -203,8 +198,7 @@ nshb_status run_scale(const nshb_tensor *src, const nshb_tensor *dst, int32_t n,
   for (int32_t i = 0; i < n;) {
     TensParams p;
     std::memset(static_cast<TensHead *>(&p), 0, sizeof(TensHead));
-    const nshb_status e = fill_launch(src, dst ? dst : src, n, i, p, nullptr);
-    if (e != NSHB_OK) return e;
+    fill_launch(src, dst ? dst : src, n, i, p, nullptr);
     p.factor = factor;
     if (w && n_rec >= 0) {
       p.coef_rec = w->rec;
@@ -226,8 +220,7 @@ nshb_status run_largest(const nshb_tensor *t, int32_t n, const TensWorkspace &w,
   int32_t i = 0;
   TensParams p;
   std::memset(static_cast<TensHead *>(&p), 0, sizeof(TensHead));
-  const nshb_status e = fill_launch(t, nullptr, n, i, p, nullptr);
-  if (e != NSHB_OK) return e;
+  fill_launch(t, nullptr, n, i, p, nullptr);
   if (i != n) return NSHB_ERR_UNSUPPORTED;
   p.rec = w.rec;
   p.kind = kNormFinite;

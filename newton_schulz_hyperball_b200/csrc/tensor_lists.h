@@ -18,6 +18,7 @@
 
 namespace nshb {
 
+constexpr int64_t kMaxRuns = 1LL << 30;   // rows that do not follow one another
 constexpr int kMaxTensCtas = 1024;   // records per launch: at most this many CTAs + kMaxTens
 
 // The workspace of a call on a list of tensors: [0, 256) the status word and the running value of

@@ -25,3 +25,19 @@ def size(t):
 @pytest.mark.parametrize("rows", [0, 1])
 def test_the_leading_dimension_of_one_row_is_not_looked_at(rows, ld):
     assert size(fake((5, 7, 7), (rows, 5, ld))) == nshb.NSHB_OK
+
+
+BIG = (1 << 30) + 1
+
+
+def test_rows_apart_from_one_another_have_a_limit_and_it_is_met_before_any_launch():
+    small, big = (5, 7, 7), (BIG, 1, 2)
+    lib = nshb.lib()
+    t, good = fake(*[small] * 600, big), fake(*[small] * 600, (BIG, 1, 1), base=1 << 40)   # the big one in a second launch
+    n = len(t)
+    assert size(t) == nshb.NSHB_ERR_UNSUPPORTED and size(good) == nshb.NSHB_OK
+    assert lib.nshb_grad_norm(t, n, 0, 1.0, TOTAL, None, WS, 1 << 20, None) == nshb.NSHB_ERR_UNSUPPORTED
+    for args in ((t, None), (t, good), (good, t)):
+        assert lib.nshb_clip_grads(*args, n, 0, 1.0, TOTAL, WS, 1 << 20, None) == nshb.NSHB_ERR_UNSUPPORTED
+        assert lib.nshb_scale_grads(*args, n, TOTAL, None) == nshb.NSHB_ERR_UNSUPPORTED
+    assert size(fake((1 << 30, 1, 2))) == size(fake((1 << 40, 1, 1))) == nshb.NSHB_OK
