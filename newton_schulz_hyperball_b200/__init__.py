@@ -307,7 +307,7 @@ def step_scaled(op: int, mats, p, factor, ws, stream=None):
     import torch
     _device_arg(factor, "factor", torch.float32, 1)
     w = _first_weight(mats)
-    if w is not None and not isinstance(factor, int) and factor.device != w.device:
+    if w is not None and isinstance(factor, torch.Tensor) and factor.device != w.device:
         raise ValueError(f"factor is on {factor.device}, the matrices on {w.device}")
     _check_rho(p, _n(mats))
     ptr, nbytes = _ws(ws)
