@@ -334,7 +334,8 @@ nshb_status nshb_scale_grads(const nshb_tensor *src, const nshb_tensor *dst, int
  *               rounded to E4M3.
  * value = code * scale (* *global).  A code is the nearest to x / (scale * *global), ties to the even
  * code, exactly (no intermediate rounding decides).  A block with a NaN or infinity gets the scale
- * NaN and zero codes; it does not count for *global.  Subnormal inputs are read as they are.
+ * NaN and zero codes; the largest magnitude that decides *global is that of all finite elements.
+ * Subnormal inputs are read as they are.
  *
  * codes:  rows of round_up(cols, 128) / 2 bytes, column 2j in the low half of byte j; 16-byte
  *         aligned; zero past cols.

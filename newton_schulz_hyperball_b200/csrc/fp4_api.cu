@@ -187,8 +187,8 @@ nshb_status run_fp4_products(const nshb_fp4 *A, const nshb_fp4 *B, const nshb_te
         const nshb_fp4 &P = s.swap ? b : a, &Q = s.swap ? a : b;
         if (kt) {
           const bool pair = s.bn == kFp4PairBn;
-          cudaError_t e = encode_fp4_maps(&q.pc, &q.ps, P, 128, 1, 1);
-          if (e == cudaSuccess) e = encode_fp4_maps(&q.qc, &q.qs, Q, pair ? 128 : s.bn, 1, pair ? 2 : 1);
+          cudaError_t e = encode_fp4_maps(&q.pc, &q.ps, P, 128, 1);
+          if (e == cudaSuccess) e = encode_fp4_maps(&q.qc, &q.qs, Q, pair ? 128 : s.bn, pair ? 2 : 1);
           if (e != cudaSuccess) {
             record_cuda_error(e);
             return NSHB_ERR_CUDA;
