@@ -1,7 +1,10 @@
 // C entry points on 4-bit matrices: argument checks and launches.  Host code only.
+#include <cuda.h>
+#include <cudaTypedefs.h>
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <atomic>
 #include <cstring>
 
 #include "../../include/nshb.h"
@@ -61,6 +64,48 @@ nshb_status check_pairs(const nshb_tensor *x, const nshb_fp4 *q, int32_t n, bool
       return NSHB_ERR_SHAPE;
   }
   return NSHB_OK;
+}
+
+// The driver's tensor-map encoder, looked up once.
+cudaError_t find_encoder(PFN_cuTensorMapEncodeTiled_v12000 *encode) {
+  static std::atomic<void *> kept{nullptr};
+  void *fn = kept.load(std::memory_order_acquire);
+  if (!fn) {
+    cudaDriverEntryPointQueryResult found;
+    const cudaError_t e = cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &fn, cudaEnableDefault, &found);
+    if (e != cudaSuccess) return e;
+    if (found != cudaDriverEntryPointSuccess || !fn) return cudaErrorNotSupported;
+    kept.store(fn, std::memory_order_release);
+  }
+  *encode = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn);
+  return cudaSuccess;
+}
+
+// Tensor maps of a 4-bit matrix for the products: boxes of `rows` rows of codes and of `row_tiles` row tiles of
+// scales, a step of 256 columns wide.
+cudaError_t encode_maps(CUtensorMap *codes, CUtensorMap *scales, const nshb_fp4 &q, int rows, int row_tiles) {
+  PFN_cuTensorMapEncodeTiled_v12000 encode = nullptr;
+  const cudaError_t e = find_encoder(&encode);
+  if (e != cudaSuccess) return e;
+  const cuuint64_t kp = (cuuint64_t)(q.cols + 127) / 128 * 128;
+  const bool nv = q.format == NSHB_NVFP4;
+  const cuuint32_t ones[3] = {1, 1, 1};
+  {
+    const cuuint64_t dims[2] = {kp / 2, (cuuint64_t)q.rows};
+    const cuuint64_t strides[1] = {kp / 2};
+    const cuuint32_t box[2] = {128, (cuuint32_t)rows};
+    if (encode(codes, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, q.codes, dims, strides, box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE,
+               CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+      return cudaErrorInvalidValue;
+  }
+  const cuuint64_t kt = kp / (nv ? 64 : 128), rt = (cuuint64_t)(q.rows + 127) / 128;
+  const cuuint64_t dims[3] = {128, kt, rt};
+  const cuuint64_t strides[2] = {512, kt * 512};
+  const cuuint32_t box[3] = {128, nv ? 4u : 2u, (cuuint32_t)row_tiles};
+  if (encode(scales, CU_TENSOR_MAP_DATA_TYPE_UINT32, 3, q.scales, dims, strides, box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE,
+             CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+    return cudaErrorInvalidValue;
+  return cudaSuccess;
 }
 
 // How one product is laid over the GPU.
@@ -187,8 +232,8 @@ nshb_status run_fp4_products(const nshb_fp4 *A, const nshb_fp4 *B, const nshb_te
         const nshb_fp4 &P = s.swap ? b : a, &Q = s.swap ? a : b;
         if (kt) {
           const bool pair = s.bn == kFp4PairBn;
-          cudaError_t e = encode_fp4_maps(&q.pc, &q.ps, P, 128, 1);
-          if (e == cudaSuccess) e = encode_fp4_maps(&q.qc, &q.qs, Q, pair ? 128 : s.bn, pair ? 2 : 1);
+          cudaError_t e = encode_maps(&q.pc, &q.ps, P, 128, 1);
+          if (e == cudaSuccess) e = encode_maps(&q.qc, &q.qs, Q, pair ? 128 : s.bn, pair ? 2 : 1);
           if (e != cudaSuccess) {
             record_cuda_error(e);
             return NSHB_ERR_CUDA;

@@ -532,31 +532,6 @@ cudaError_t encode_z_tensor_map(CUtensorMap *map, const void *z, int64_t d, int6
   return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
-cudaError_t encode_fp4_maps(CUtensorMap *codes, CUtensorMap *scales, const nshb_fp4 &q, int rows, int row_tiles) {
-  cudaError_t e = load_encoder();
-  if (e != cudaSuccess) return e;
-  const cuuint64_t kp = (cuuint64_t)(q.cols + 127) / 128 * 128;
-  const bool nv = q.format == NSHB_NVFP4;
-  const cuuint32_t ones[3] = {1, 1, 1};
-  {
-    const cuuint64_t dims[2] = {kp / 2, (cuuint64_t)q.rows};
-    const cuuint64_t strides[1] = {kp / 2};
-    const cuuint32_t box[2] = {128, (cuuint32_t)rows};
-    CUresult r = g_encode(codes, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, q.codes, dims, strides, box, ones,
-                          CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-    if (r != CUDA_SUCCESS) return cudaErrorInvalidValue;
-  }
-  const cuuint64_t kt = kp / (nv ? 64 : 128), rt = (cuuint64_t)(q.rows + 127) / 128;
-  const cuuint64_t dims[3] = {128, kt, rt};
-  const cuuint64_t strides[2] = {512, kt * 512};
-  const cuuint32_t box[3] = {128, nv ? 4u : 2u, (cuuint32_t)row_tiles};
-  CUresult r = g_encode(scales, CU_TENSOR_MAP_DATA_TYPE_UINT32, 3, q.scales, dims, strides, box, ones,
-                        CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-  return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
-}
-
 namespace {
 
 int set_up_device(int dev, int num_sms, cudaError_t *err) {

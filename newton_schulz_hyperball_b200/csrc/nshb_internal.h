@@ -526,9 +526,6 @@ cudaError_t launch_fp4_dequantize(const Fp4Params &p, cudaStream_t s);
 // 256 rows of P (split 1, kt > 0, kFp4DTrans unset).
 constexpr int kFp4PairBn = 256;
 cudaError_t launch_fp4_gemm(const Fp4GemmParams &p, int bn, int split, bool nv, cudaStream_t s);
-// Tensor maps of a 4-bit matrix for the products: boxes of `rows` rows of codes and of `row_tiles` row tiles of
-// scales, a step of 256 columns wide.
-cudaError_t encode_fp4_maps(CUtensorMap *codes, CUtensorMap *scales, const nshb_fp4 &q, int rows, int row_tiles);
 
 constexpr size_t kMaxParamBytes = 32764;   // kernel parameter limit (CUDA 12.1+, sm_70+)
 static_assert(sizeof(MomentumParams) <= kMaxParamBytes, "MomentumParams");
