@@ -303,8 +303,8 @@ typedef enum { NSHB_NORM_L2 = 0, NSHB_NORM_INF = 1 } nshb_norm_kind;
  *   total[0] = norm;  total[1] = min(1, max_norm / (norm + 1e-6)), the factor that clips to max_norm
  *   each[i]  = the norm of tensor i (each may be NULL)
  * in fp32 into the DEVICE arrays total (2 floats) and each (n floats).  The same inputs give
- * the same bits on every call.  An infinite element gives an infinite norm and the factor 0, a NaN
- * gives NaN for both; either sets NSHB_DEV_NONFINITE in the workspace's status word, which the
+ * the same bits on every call.  An infinite element, or a norm above fp32's largest number, gives an infinite
+ * norm and the factor 0, a NaN gives NaN for both; either sets NSHB_DEV_NONFINITE in the workspace's status word, which the
  * call clears otherwise.  max_norm > 0 (infinity: the factor is 1 for every finite norm). */
 nshb_status nshb_grad_norm(const nshb_tensor *g, int32_t n, int32_t kind, float max_norm, float *total, float *each,
                            void *ws, size_t ws_bytes, nshb_stream stream);

@@ -8,14 +8,18 @@
 // every 512-byte tile of scales is moved whole.  A lane takes 8 columns, 16 lanes a row: each load and store
 // instruction of a warp covers two whole pieces of rows.  The CTAs are persistent and load ahead: a batch
 // of rows of the same or the next tile is under way while one is processed.  Four bf16 6144 x 2048
-// matrices: to MXFP4 in 21.4 us (127 MB, 5.9 TB/s; instruction issue 0.66 a clock is the next bound: 28.9 us
-// before whole tiles lost their bounds checks and bf16 its widening), their values in 22.7 us (23.3 with a load for each scale).
+// matrices: to MXFP4 in 21.7 us (127 MB, 5.9 TB/s; instruction issue 0.66 a clock is the next bound: 28.9 us
+// before whole tiles lost their bounds checks and bf16 its widening), their values in 22.8 us (0.6 more with a load for each scale).
 //
 // For the transpose the tile goes through shared memory as 32-bit words, whose place is permuted by
 // the 32-row group (word ^ 8 group), so that the four groups of eight columns that a warp reads
-// fall into different banks.  8192 x 2048 bf16 to NVFP4: 15.8 us, 7 of them the pass for the largest
-// magnitude, which the matrix's scale needs before the first code.  Instruction issue bounds the other pass (16.7
-// an element and 12.5 us before whole tiles lost their bounds checks and bf16 its fp32 quotients).
+// fall into different banks.  8192 x 2048 bf16 to NVFP4: 16.0 us (14.1 plain, MXFP4 8.2 and 7.4), 6.6 of them the pass for
+// the largest magnitude, which the matrix's scale needs before the first code.  Instruction issue bounds the other pass
+// (16.7 an element and 12.5 us before whole tiles lost their bounds checks and bf16 its fp32 quotients).  Three
+// matrices in turn, so that none is in the L2 cache as a whole: bf16 20.8 us (19.0, 11.8, 9.3), fp32 45.0 us (41.1, 16.5,
+// 14.1): a quotient of fp32 numbers is divided and corrected to the last bit.
+//
+// The occupancies below leave some instances a register or two short (4 to 16 bytes spilled: bf16 transposed, fp32 MXFP4).
 #include <cuda_runtime.h>
 
 #include <type_traits>

@@ -140,17 +140,17 @@ Shape shape_of(int64_t m, int64_t n, int64_t kt, bool sym, bool pairs, bool narr
   }
   s.tiles = count_tiles(p, q, 128, s.bn, sym);
   // A step of 256 columns takes a lone CTA 0.3 us, joining the parts of a cluster 2 us (narrow tiles) to 4 us
-  // (128 x 128): split long sums of few tiles.  Measured: 1 x 2048 x 6144 in 8.5 us with 1 CTA a tile, 5.0 with
-  // 4, 4.5 with 8; 128 x 2048 x 8192 in 13.3, 8.7 and 9.9 us; but 1 x 6144 x 2048 in 4.1 and 4.8 us,
-  // 1024^3 in 5.2 and 9.1 us with 1 and 4.
+  // (128 x 128): split long sums of few tiles.  Measured with 1, 2, 4 and 8 CTAs a tile (NVFP4 to bf16, us): 1 x 2048 x 6144
+  // 9.5, 7.2, 5.6, 5.4; 64 x 2048 x 6144 11.1, 8.8, 7.0, 7.3; 128 x 2048 x 8192 13.1, 11.8, 8.6, 10.4; but
+  // 1 x 6144 x 2048 4.7, 5.2, 5.2, 9.5; 64 x 6144 x 2048 6.3, 6.8, 7.5, 12.5; 1024^3 5.0, 8.2, 9.5, 20.8.
   const bool wide_tile = s.bn == 128;
   if (kt >= (wide_tile ? 32 : 24) && s.tiles * 8 <= (wide_tile ? sms / 2 : sms)) s.split = 8;
   else if (kt >= 16 && s.tiles * 4 <= sms) s.split = 4;
   else if (kt >= (wide_tile ? 32 : 16) && s.tiles * 2 <= sms) s.split = 2;
   // Few tiles without a cluster: half as wide ones spread the epilogue over twice the CTAs.  Measured (128 and 64
-  // columns): 1000 x 777 x 1333 to fp32 8.5 and 7.0 us, 768 x 768 x 1000 6.8 and 5.8 us, its Gram matrix 7.6 and
-  // 7.0 us, 1024^3 to bf16 4.9 and 4.6 us; two CTAs of an SM hide each other's epilogue as well: eight of 512 x 512 x
-  // 2048 (256 tiles) 7.6 and 6.8 us, but in two waves 16 of them 8.5 and 12.9 us.
+  // columns): 1000 x 777 x 1333 to fp32 8.3 and 6.8 us, 768 x 768 x 1000 5.2 and 4.4 us, the Gram matrix of 768 x 1000 7.8 and
+  // 5.9 us, 1024^3 to bf16 5.6 and 4.9 us; two CTAs of an SM hide each other's epilogue as well: eight of 512 x 512 x
+  // 2048 (256 tiles) 7.9 and 7.0 us, but in two waves 16 of them 9.8 and 14.7 us.
   if (narrow && wide_tile && s.split == 1) {
     s.bn = 64;
     s.tiles = count_tiles(p, q, 128, 64, sym);
@@ -189,9 +189,14 @@ nshb_status run_fp4_products(const nshb_fp4 *A, const nshb_fp4 *B, const nshb_te
       wide += s.bn == kFp4PairBn ? s.tiles : 0;
       few += t.tiles * t.split;
     }
+  // CTA pairs where their tiles are half as many as the SMs, so that every SM has work.  Measured (single CTAs and pairs):
+  // 1024 x 6144 x 2048 (96 pair tiles) 14.6 and 11.9 us, 2304 x 2304 x 2048 (81) 14.0 and 11.4 us, Gram matrices of three
+  // 2048 x 8192 inputs (108) 42.4 and 33.6 us; below the border 2048^3 (64) 9.0 and 9.0 us, 1536 x 1536 x 2048 (36) 6.8 and
+  // 8.2 us, one such Gram matrix (36) 18.5 and 19.3 us, 1024^3 (16) 4.7 and 7.0 us; but two (72) 24.1 and 21.9 us and
+  // 2048 x 2048 x 6144 (64) 17.3 and 14.1 us: for long sums the border is too high.
   const bool pairs = wide >= sms / 2, narrow = few <= 2 * sms;
-  // A launch takes the products of one kind (shape and format), wherever they stand in the list: 32 products of four
-  // kinds in turn take 50 us, in launches of neighbours 147 us.
+  // A launch takes the products of one kind (shape and format), wherever they stand in the list: 130 x 140 x 64, 1 x 200 x
+  // 300, 40 x 130 x 5000 and 700 x 800 x 256 in turn, eight times, take 23 us, in a launch each 126 us.
   auto log2 = [](int v) {
     int k = 0;
     while (v >>= 1) ++k;

@@ -10,9 +10,10 @@
 //
 // One CTA computes 128 rows of P x BN rows of Q.  Few rows on one side (single tokens) are bound by
 // the bytes of the other operand: that one takes the 128 lanes, BN is as small as the rows allow,
-// and a cluster of up to 8 CTAs shares the columns of one tile, each summing its part; the parts are joined
-// through distributed shared memory in a fixed order.  One token through 6144 x 2048 NVFP4: 4.5 us (7.1 MB,
-// bound by latency: 8 dependent steps of 0.3 us, of which each CTA's ring holds 5).
+// and a cluster of up to 8 CTAs shares the columns of a tile whose sum is long, each summing its part; the parts are
+// joined through distributed shared memory in a fixed order.  One token through 6144 x 2048 NVFP4: 4.8 us for 7.1 MB,
+// bound by latency: 48 CTAs, each with 5 of its 8 steps of loads under way at once (a ring of 110 KB, so that larger
+// calls have two CTAs on an SM).
 //
 // Enough 256 x 256 tiles to fill the GPU go to CTA pairs (fp4_pair_kernel): a pair reads 64 bytes of
 // codes per clock and SM for the work that single CTAs with 128 x 128 tiles need 128 for.
@@ -502,9 +503,9 @@ __global__ void __launch_bounds__(kThreads, 2) fp4_gemm_kernel(const __grid_cons
   }
 }
 
-// 256 x 256 tiles on CTA pairs, persistent.  8192^3: 177 us MXFP4, 184 us NVFP4 (6.2 and 6.0 PFLOP/s); 8192 x 6144 x 2048
-// NVFP4 to bf16: 48 us (57 with operands and result in DRAM), tensor pipe 50 %; four 2048 x 8192 Gram
-// matrices MXFP4 to fp32: 38 us.  A step of 256 columns is 513 clocks of MMAs and took 600 to 660 in the
+// 256 x 256 tiles on CTA pairs, persistent.  8192^3: 180 us MXFP4, 186 us NVFP4 (6.1 and 5.9 PFLOP/s, up to 216 us under the
+// power cap); 8192 x 6144 x 2048 NVFP4 to bf16: 47 us (57 with operands and result in DRAM), tensor pipe 58 %; four
+// 2048 x 8192 Gram matrices MXFP4 to fp32: 36 us.  A step of 256 columns is 513 clocks of MMAs and took 600 to 660 in the
 // long sums; what is left is the 870 clocks in which a tile waits for the shared columns below, and the last
 // tile's epilogue (2 us in bf16, 7 us for an fp32 block with its mirror image).
 //
@@ -514,8 +515,9 @@ __global__ void __launch_bounds__(kThreads, 2) fp4_gemm_kernel(const __grid_cons
 //
 // The MMA warp copies a step's scales into tensor memory ahead of its MMAs: 24 (MX) or 48 columns, a third for this
 // CTA's rows of P, the others for all rows of Q.  Copies and MMAs of one thread run in order and
-// overlap.  (8192 x 6144 x 2048 NVFP4 took 83 us with `lane == 0` code instead of an elected lane, 63 us with
-// that and four more warps for the copies, 65 us with them and 256 x 192 tiles.)
+// overlap.  (8192 x 6144 x 2048 NVFP4 took 83 us with `lane == 0` code instead of an elected lane.  Under `lane == 0`,
+// four more warps for the copies made it 63 us, and 256 x 192 tiles with two whole accumulators 65 us; neither has been
+// timed with an elected lane.)
 template <bool NV>
 struct PairCfg {
   static constexpr int kBn = kFp4PairBn;
