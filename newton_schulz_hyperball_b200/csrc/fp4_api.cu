@@ -301,10 +301,12 @@ nshb_status nshb_fp4_quantize(const nshb_tensor *X, const nshb_fp4 *Q, int32_t n
     std::memset(static_cast<Fp4Head *>(&p), 0, sizeof(Fp4Head));
     nshb_tensor src[kMaxFp4];     // the NVFP4 items' sources, whose largest magnitudes come first
     int32_t of[kMaxFp4], n_src = 0;
-    int64_t tiles = 0;
+    int64_t tiles = 0, windows = 0;
     for (; i < n && p.n < kMaxFp4; ++i) {
       if (Q[i].rows == 0 || Q[i].cols == 0) continue;
       if (p.n && another_kind(X[i], Q[i], p.item[0])) break;
+      windows += X[i].rows * (X[i].cols / (kWinBytes / 4) + 2);     // of run_largest, at most
+      if (p.n && windows > kMaxWindows) break;
       if (!fill_item(Q[i], X[i], tiles, p.item[p.n])) {
         if (p.n == 0) return NSHB_ERR_UNSUPPORTED;
         break;

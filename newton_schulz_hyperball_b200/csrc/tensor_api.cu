@@ -86,7 +86,7 @@ bool fill(const nshb_tensor &s, const nshb_tensor *d, int64_t &win, TensRec &q) 
     q.per_row = (int32_t)(per / cols);
     n = (rows + q.per_row - 1) / q.per_row;
   }
-  if (win + n > (1LL << 30)) return false;
+  if (win + n > kMaxWindows) return false;
   q.rows = (int32_t)rows;
   win += n;
   return true;
@@ -221,7 +221,6 @@ nshb_status run_largest(const nshb_tensor *t, int32_t n, const TensWorkspace &w,
   TensParams p;
   std::memset(static_cast<TensHead *>(&p), 0, sizeof(TensHead));
   fill_launch(t, nullptr, n, i, p, nullptr);
-  if (i != n) return NSHB_ERR_UNSUPPORTED;
   p.rec = w.rec;
   p.kind = kNormFinite;
   for (int k = 0; k < p.ntens; ++k) {

@@ -19,6 +19,7 @@
 namespace nshb {
 
 constexpr int64_t kMaxRuns = 1LL << 30;   // rows that do not follow one another
+constexpr int64_t kMaxWindows = 1LL << 30;   // of a launch
 constexpr int kMaxTensCtas = 1024;   // records per launch: at most this many CTAs + kMaxTens
 
 // The workspace of a call on a list of tensors: [0, 256) the status word and the running value of
@@ -34,8 +35,8 @@ nshb_status check_tens_ws(void *ws, size_t bytes, int32_t n);
 nshb_status check_tensor(const nshb_tensor &t);
 nshb_status check_tensors(const nshb_tensor *t, int32_t n);
 int tens_ctas(int nwin);
-// The largest finite magnitude of each of up to kMaxTens tensors with elements, left as records: tensor k's
-// are w.rec[rec_begin[k]] .. [+ n_rec[k]), each the bits of a magnitude as a double.
+// The largest finite magnitude of each of up to kMaxTens tensors with elements and kMaxWindows windows, left as
+// records: tensor k's are w.rec[rec_begin[k]] .. [+ n_rec[k]), each the bits of a magnitude as a double.
 nshb_status run_largest(const nshb_tensor *t, int32_t n, const TensWorkspace &w, cudaStream_t st, int32_t *rec_begin,
                         int32_t *n_rec);
 constexpr int64_t kMaxFp4Dim = 1LL << 24;

@@ -41,3 +41,17 @@ def test_rows_apart_from_one_another_have_a_limit_and_it_is_met_before_any_launc
         assert lib.nshb_clip_grads(*args, n, 0, 1.0, TOTAL, WS, 1 << 20, None) == nshb.NSHB_ERR_UNSUPPORTED
         assert lib.nshb_scale_grads(*args, n, TOTAL, None) == nshb.NSHB_ERR_UNSUPPORTED
     assert size(fake((1 << 30, 1, 2))) == size(fake((1 << 40, 1, 1))) == nshb.NSHB_OK
+
+
+def test_a_quantisation_of_more_than_one_launchs_windows_is_not_refused():
+    """65 strided sources of 2^24 rows: more than 2^30 pieces for the pass that finds the largest magnitudes."""
+    import torch
+    if torch.cuda.is_available():
+        pytest.skip("the pointers are made up: only where nothing can be launched")
+    n = 65
+    x = fake(*[(1 << 24, 256, 257)] * n)
+    q = (nshb.nshb_fp4 * n)()
+    for i in range(n):
+        q[i].rows, q[i].cols, q[i].format = 1 << 24, 256, nshb.NSHB_NVFP4
+        q[i].codes, q[i].scales, q[i].global_ = 0x40000000, 0x50000000, 0x60000000
+    assert nshb.lib().nshb_fp4_quantize(x, q, n, 0, WS, 1 << 20, None) == nshb.NSHB_ERR_CUDA    # no GPU to launch on
